@@ -20,6 +20,7 @@ __all__ = [
     "kernel_timing", "kernel_time", "launch_count", "solve_dual_scale_noalloc", "code_bytes",
     "two_level_quant", "w4a4_gemm", "scale_tiles", "solve_dual_scale_batched_host", "copy_streams",
     "SolveGraph", "solve_dual_scale_batched_graph", "col_row_block", "col_partials", "col_finalize",
+    "add_rmsnorm_quant", "kv_cache", "kv_append", "kv_read", "kv_attention", "kv_attention_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -623,3 +624,7 @@ def launch_count() -> int:
 def last_device_status(stream=None) -> int:
     """Synchronise and return (and clear) the device flags as a dq status code."""
     return lib().dq_last_device_status(_stream(stream))
+
+
+from .serving import (SERVING_EXPORTS, add_rmsnorm_quant, kv_append, kv_attention,  # noqa: E402
+                      kv_attention_workspace, kv_cache, kv_read)

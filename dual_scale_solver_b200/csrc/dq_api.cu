@@ -27,6 +27,7 @@
 #include "../../include/dq.h"
 #define DQ_DEFINE_HOST_KERNELS
 #include "dq_launch.h"
+#include "dq_serving.h"
 
 using namespace dq;
 
@@ -714,6 +715,22 @@ __global__ void dequant_kernel(const uint8_t *codes, const void *gs, int64_t row
 
 }  // namespace
 
+// what the serving operators (dq_serving_api.cu) take from this unit
+namespace dq {
+
+unsigned int *serving_status_word() { return status_ptr(); }
+
+void serving_count_launches(int k) { count_launches(k); }
+
+dq_status serving_format(const dq_format *f, int *bits) {
+    FmtInfo fi;
+    const dq_status s = check_format(f, &fi);
+    if (s == DQ_OK && bits) *bits = fi.bits;
+    return s;
+}
+
+}  // namespace dq
+
 extern "C" {
 
 const char *dq_version(void) { return "dq 0.1.0 (sm_100a)"; }
@@ -734,6 +751,7 @@ const char *dq_strerror(dq_status s) {
             return "matrix needs more scratch than the built-in 32 MiB buffer of "
                    "dq_solve_dual_scale_noalloc holds";
         case DQ_ERR_TIMEOUT: return "a kernel's bounded wait ran out (stalled pipeline)";
+        case DQ_ERR_INDEX: return "a sequence start, length or page index out of range";
     }
     return "unknown status";
 }
@@ -1290,6 +1308,7 @@ dq_status dq_last_device_status(dq_stream stream) {
     DQ_CUDA(cudaMemcpy(p, &zero, sizeof(zero), cudaMemcpyHostToDevice));
     if (v & STATUS_TIMEOUT) return DQ_ERR_TIMEOUT;  // a kernel's bounded wait ran out
     if (v & STATUS_NONFINITE) return DQ_ERR_NONFINITE;
+    if (v & STATUS_INDEX) return DQ_ERR_INDEX;
     if (v & STATUS_RANGE) return DQ_ERR_RANGE;
     return DQ_OK;
 }

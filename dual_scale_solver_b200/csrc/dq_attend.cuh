@@ -1,0 +1,899 @@
+// dq_attend.cuh — attention of few query rows over the 4-bit cache.
+//
+//   out = softmax(scale q . k_hat) v_hat,  k_hat = c_k s_k,  v_hat = c_v s_v
+//
+// For single tokens (and drafts of a few) the work is the streaming of codes:
+// each code byte is used for at most 8 NB query rows.  Tensor-core products
+// keep the arithmetic per code low enough to stay near the memory's pace:
+//
+//  S^T = K Q^T   A = 16 tokens x 16 channels of codes as fp16 (exact), B = 8
+//                query rows as fp16, scaled by a power of two per row (exact
+//                but for elements 2^-38 below the row's largest); float32
+//                accumulation per group of G channels, then one multiply-add
+//                with the group's scale.
+//  O^T = V^T P^T A = 16 channels x 16 tokens of codes as fp16, B = the
+//                probabilities times the tokens' group scales, fp16.  The
+//                power of two of a tile's largest value scale is part of the
+//                running maximum (p s lies in [0, 2^15)), so fp16's range of
+//                2^39 below it holds the rest: rounding 2^-12 per term,
+//                below the output type's own 2^-9.
+//
+// A query row is one (token, head of the group) pair, so the g heads of a
+// group share every code.  The probabilities pass from the layout of the
+// first product's result to the second's operand with movmatrix.
+//
+// Work: (sequence, cache head, tile of 8 NB rows) segments of 256-token
+// units, numbered through the batch; CTA i of n takes units [U i / n, U (i+1)
+// / n) (found by a scan over the sequences' lengths on the device, so lengths
+// may differ freely and the call needs no host copy of them).  A segment that
+// one CTA covers is written at once; the pieces of one that is cut go to the
+// workspace, at most two per CTA, and a second kernel joins them in order.
+// A warp takes 32 tokens at a time through its own cp.async ring.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "dq_kv.cuh"
+
+namespace dq {
+
+constexpr int kAttWarps = 8;
+constexpr int kAttThreads = 32 * kAttWarps;
+constexpr int kAttTile = 32;                       // tokens per warp step
+constexpr int kAttUnit = kAttTile * kAttWarps;     // tokens per unit
+constexpr int kAttCtas = 2 * 148;
+constexpr int kAttRowsMax = 16;
+
+// What CTA i leaves for the joining kernel: the segment that starts (and
+// does not end) in its share.
+struct AttMeta {
+    long long end;          // global number of the segment's last unit, plus 1
+    long long units;        // units of the whole batch
+    int seq, seg;           // seq < 0: nothing to join
+};
+
+struct AttArgs {
+    const uint16_t *q;
+    int64_t q_token, q_head;
+    uint16_t *out;
+    int64_t out_token, out_head;
+    int64_t tokens;
+    int group;              // query heads per cache head
+    float scale_log2;       // scale * log2(e)
+    int causal;
+    dq_kv_cache cache;
+    dq_kv_batch batch;
+    float *part;            // [2 n][rows][D]
+    float2 *part_ml;        // [2 n][rows]  (running maximum, sum)
+    AttMeta *meta;          // [n]
+    unsigned int *status;
+};
+
+struct AttSpan {            // a sequence's segments and units
+    int qt;                 // row tiles
+    int kvt;                // units per segment
+    long long units;
+};
+
+template <int ROWS>
+__device__ __forceinline__ AttSpan att_span(const KvSeq &s, int group, int heads) {
+    AttSpan a;
+    a.qt = (int)(((long long)s.n * group + ROWS - 1) / ROWS);
+    a.kvt = max(1, (s.len + kAttUnit - 1) / kAttUnit);
+    a.units = (long long)a.qt * heads * a.kvt;
+    return a;
+}
+
+// ---- small wrappers
+__device__ __forceinline__ uint32_t att_smem(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t (&w)[4], uint32_t addr) {
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+// (x & m) | (y & ~m)
+__device__ __forceinline__ uint32_t bit_select(uint32_t x, uint32_t y, uint32_t m) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(x), "r"(y), "r"(m));
+    return r;
+}
+// (x & m) | v
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t v) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight INT4 codes of a word: out[i] holds nibbles i (low) and i + 4 (high)
+// as fp16.  With u = c + 8, 0x6400 | u is 1024 + u; for the nibbles in bits 4
+// to 7 it is 1024 + 16 u, brought down by a multiply-add; all exact.
+__device__ __forceinline__ void int4_halves(uint32_t w, uint32_t (&out)[4]) {
+    const uint32_t u = w ^ 0x88888888u, u8 = u >> 8;
+    out[0] = hsub2(and_or(u, 0x000F000Fu, 0x64006400u), 0x64086408u);
+    out[1] = hfma2(and_or(u, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);   // / 16, - 72
+    out[2] = hsub2(and_or(u8, 0x000F000Fu, 0x64006400u), 0x64086408u);
+    out[3] = hfma2(and_or(u8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);
+}
+// Eight E2M1 codes of a word by bytes: out[i] holds nibbles 2i (low) and 2i + 1.
+__device__ __forceinline__ void e2m1_bytes(uint32_t w, uint32_t (&out)[4]) {
+    asm("{ .reg .b8 p, q, r, s; mov.b32 {p, q, r, s}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, p; cvt.rn.f16x2.e2m1x2 %1, q;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, r; cvt.rn.f16x2.e2m1x2 %3, s; }"
+        : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3]) : "r"(w));
+}
+// Two halves of 4 nibbles each (a token each): out[i] holds nibble i of the
+// low half and nibble i of the high half.
+template <int CODES>
+__device__ __forceinline__ void nibble_pairs(uint32_t x, uint32_t (&out)[4]) {
+    if constexpr (CODES == CODES_INT4) {
+        int4_halves(x, out);
+    } else {
+        const uint32_t z = bit_select(x, x >> 12, 0x0F0F0F0Fu);      // bytes 0, 1: nibbles 0, 2
+        const uint32_t w = bit_select(x >> 4, x >> 16, 0x0F0F0F0Fu); // bytes 0, 1: nibbles 1, 3
+        asm("{ .reg .b8 p, q, r, s, t; mov.b32 {p, q, t, t}, %4; mov.b32 {r, s, t, t}, %5;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, p; cvt.rn.f16x2.e2m1x2 %2, q;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, r; cvt.rn.f16x2.e2m1x2 %3, s; }"
+            : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3]) : "r"(z), "r"(w));
+    }
+}
+
+// A token's group scales in shared memory: SB bytes as words.
+template <int SB>
+struct ScaleWords {
+    static constexpr int N = SB < 4 ? 1 : SB / 4;
+    uint32_t w[N];
+    __device__ __forceinline__ void load(const uint8_t *p) {
+        if constexpr (SB == 1) w[0] = *p;
+        else if constexpr (SB == 2) w[0] = *reinterpret_cast<const uint16_t *>(p);
+        else if constexpr (SB == 4) w[0] = *reinterpret_cast<const uint32_t *>(p);
+        else if constexpr (SB == 8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        }
+    }
+    // Scale of group g (a constant after unrolling).
+    template <int GS>
+    __device__ __forceinline__ float get(int g) const {
+        if constexpr (GS == SC_BF16) {
+            const uint32_t v = w[g / 2];
+            return __uint_as_float((g & 1) ? (v & 0xFFFF0000u) : (v << 16));
+        } else if constexpr (GS == SC_E8M0) {
+            const uint32_t v = w[g / 4];
+            const int b = g % 4;
+            return __uint_as_float((b == 3 ? v >> 1 : v << (23 - 8 * b)) & 0x7F800000u);
+        } else {
+            const uint16_t v = (uint16_t)((g & 2) ? (w[g / 4] >> 16) : w[g / 4]);
+            uint32_t h2;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(v));
+            float f;
+            if (g & 1) asm("{ .reg .f16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, h; }" : "=f"(f) : "r"(h2));
+            else asm("{ .reg .f16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l; }" : "=f"(f) : "r"(h2));
+            return f;
+        }
+    }
+    // floor(log2) of the largest scale (E4M3: at least its normal range's);
+    // -200 if all are zero.
+    template <int GS>
+    __device__ __forceinline__ int top() const {
+        uint32_t m = w[0];
+        if constexpr (GS == SC_BF16) {
+#pragma unroll
+            for (int i = 1; i < N; ++i) m = __vmaxu2(m, w[i]);
+            const uint32_t v = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
+            return v == 0 ? -200 : (int)(v >> 7) - 127;
+        } else {
+#pragma unroll
+            for (int i = 1; i < N; ++i) m = __vmaxu4(m, w[i]);
+            m = __vmaxu4(m, m >> 16);
+            const uint32_t v = max(m & 0xFFu, (m >> 8) & 0xFFu);
+            if constexpr (GS == SC_E8M0) return v == 0 ? -200 : (int)v - 127;
+            else return v == 0 ? -200 : max((int)((v & 0x7Fu) >> 3), 1) - 7;
+        }
+    }
+    __device__ __forceinline__ static void zero(uint8_t *p) {
+#pragma unroll
+        for (int i = 0; i < SB; ++i) p[i] = 0;
+    }
+};
+
+template <int CODES, int GS, int G, int D, int NB>
+struct AttShape {
+    static constexpr int ROWS = 8 * NB;
+    static constexpr int NG = D / G;
+    static constexpr int SB = NG * (GS == SC_BF16 ? 2 : 1);      // scale bytes of a token
+    static constexpr int CB = kAttTile * D / 2;                  // code bytes of a warp tile
+    static constexpr int TB = kAttTile * SB;                     // scale bytes of a warp tile
+    static constexpr int STAGE = 2 * CB + 2 * TB;
+    static constexpr int RING_MAX = 108 * 1024 / kAttWarps / STAGE;
+    static constexpr int RING = RING_MAX > 5 ? 5 : RING_MAX;
+    static constexpr int RING_BYTES = kAttWarps * RING * STAGE;
+    static constexpr int OST = D + 4;                            // row stride of the joining buffer
+    static constexpr int JOIN_BYTES = kAttWarps * ROWS * OST * 4;
+    static constexpr int BODY = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
+    static constexpr int BYTES = BODY + kAttWarps * ROWS * 8 + 64;
+    static_assert(RING >= 2, "ring");
+};
+
+// Byte offset of 16-byte chunk `ch` of token row `t` in a code tile: rows of
+// D / 2 bytes, chunks exchanged so that the 8 rows of an 8x8 matrix load fall
+// on different banks.
+template <int D>
+__device__ __forceinline__ uint32_t code_off(int t, int ch) {
+    if constexpr (D == 128) return (uint32_t)(t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
+    else return (uint32_t)(t * 32 + ((ch ^ ((t >> 2) & 1)) << 4));
+}
+
+template <int CODES, int GS, int G, int D, int NB>
+__global__ void __launch_bounds__(kAttThreads, NB == 1 ? 2 : 1)
+attend_split_kernel(const AttArgs A) {
+    using Sh = AttShape<CODES, GS, G, D, NB>;
+    using Sw = ScaleWords<Sh::SB>;
+    constexpr int ROWS = Sh::ROWS, RING = Sh::RING, NJ = D / 32;
+    grid_dependency_begin();
+    extern __shared__ __align__(128) uint8_t att_smem_raw[];
+    float *const join = reinterpret_cast<float *>(att_smem_raw);
+    float2 *const join_ml = reinterpret_cast<float2 *>(att_smem_raw + Sh::BODY);
+    __shared__ long long s_scan[kAttWarps + 1];
+    __shared__ long long s_first;
+    __shared__ int s_seq;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = lane >> 2, c = lane & 3;
+    const int n = gridDim.x, me = blockIdx.x;
+    const int heads = A.cache.heads, seqs = A.batch.seqs;
+
+    // ---- this CTA's share: units [u0, u1) of the batch
+    long long mine = 0, total = 0;
+    for (int b = tid; b < seqs; b += kAttThreads) {
+        const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
+        if (!s.ok && me == 0) atomicOr(A.status, STATUS_INDEX);
+        mine = att_span<ROWS>(s, A.group, heads).units;
+        total += mine;
+    }
+    const auto block_scan = [&](long long v, long long &all) {     // inclusive
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = v;
+        __syncthreads();
+        long long before = 0;
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) {
+            if (w < warp) before += s_scan[w];
+            all += s_scan[w];
+        }
+        return v + before;
+    };
+    long long units, incl = block_scan(total, units);
+    const long long u0 = units * me / n, u1 = units * (me + 1) / n;
+    if (tid == 0) {
+        AttMeta m;
+        m.end = 0;
+        m.units = units;
+        m.seq = -1;
+        m.seg = 0;
+        A.meta[me] = m;
+    }
+    if (u0 >= u1) return;
+    if (seqs <= kAttThreads) {
+        if (tid < seqs && incl - mine <= u0 && u0 < incl) {
+            s_seq = tid;
+            s_first = incl - mine;
+        }
+    } else {
+        long long base = 0;
+        for (int b0 = 0; b0 < seqs; b0 += kAttThreads) {
+            const int b = b0 + tid;
+            long long v = 0, all;
+            if (b < seqs) v = att_span<ROWS>(kv_seq(A.batch, A.cache.page_size, A.tokens, b), A.group, heads).units;
+            const long long in = base + block_scan(v, all);
+            if (v > 0 && in - v <= u0 && u0 < in) {
+                s_seq = b;
+                s_first = in - v;
+            }
+            base += all;
+            if (base > u0) break;
+        }
+    }
+    __syncthreads();
+    int seq = s_seq;
+    long long first = s_first;
+
+    uint8_t *const ring = att_smem_raw + warp * RING * Sh::STAGE;
+    const uint32_t ring_s = att_smem(ring);
+    // byte of this lane's row in a matrix load: token (lane & 7) + 8 of matrix 1, 3; chunk + 1 of 2, 3
+    const int lm_t = (lane & 7) + ((lane >> 3) & 1) * 8, lm_c = lane >> 4;
+
+    for (long long u = u0; u < u1;) {
+        const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
+        const AttSpan sp = att_span<ROWS>(s, A.group, heads);
+        if (u >= first + sp.units) {
+            first += sp.units;
+            ++seq;
+            continue;
+        }
+        const long long local = u - first;
+        const int seg = (int)(local / sp.kvt);
+        const int t0 = (int)(local - (long long)seg * sp.kvt);
+        const int t1 = (int)min((long long)sp.kvt, t0 + (u1 - u));
+        const int head = seg / sp.qt, row0 = (seg - head * sp.qt) * ROWS;
+        const int nrows = s.n * A.group;                       // of the sequence
+        const int rows = min(ROWS, nrows - row0);              // of this tile
+        // positions below limit(row) are seen by the row
+        const auto limit = [&](int row) {
+            return A.causal ? min(max(s.len - s.n + row / A.group + 1, 0), s.len) : s.len;
+        };
+        const int lim_min = limit(row0), lim_max = limit(row0 + rows - 1);
+        const int lo = t0 * kAttUnit, hi = min(t1 * kAttUnit, lim_max);
+
+        // ---- the query rows: B operands, and the factor that takes a
+        // product of scaled operands to log2 units
+        uint32_t qf[NB][NJ][4];
+        float fac[NB][2];
+        int lim[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int row = row0 + 8 * nb + r;
+            uint4 raw[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) raw[j] = make_uint4(0, 0, 0, 0);
+            if (8 * nb + r < rows) {
+                const int tok = row / A.group;
+                const uint16_t *p = A.q + (s.s0 + tok) * A.q_token +
+                                    (int64_t)(head * A.group + row - tok * A.group) * A.q_head + 8 * c;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(p + 32 * j));
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint32_t v[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = __vmaxu2(top, v[k] & 0x7FFF7FFFu);
+            }
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max((int)(top >> 7) - 127, -100);     // of the row's largest element
+            const float up = pow2f(13 - e);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint32_t v[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[2 * k] = __uint_as_float(v[k] << 16) * up;
+                    x[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u) * up;
+                }
+                if constexpr (CODES == CODES_INT4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) qf[nb][j][k] = f16x2_rn(x[k], x[k + 4]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) qf[nb][j][k] = f16x2_rn(x[2 * k], x[2 * k + 1]);
+                }
+            }
+            const float f = A.scale_log2 * pow2f(e - 13);
+            fac[nb][0] = __shfl_sync(0xffffffffu, f, 8 * c);         // row 2c of the tile
+            fac[nb][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);     // row 2c + 1
+#pragma unroll
+            for (int h = 0; h < 2; ++h) lim[nb][h] = limit(min(row0 + 8 * nb + 2 * c + h, row0 + rows - 1));
+        }
+
+        float o[NB][NJ][2][4];
+        float m[NB][2], l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[nb][j][k >> 2][k & 3] = 0.0f;
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.0f;
+        }
+        // ---- tokens, 32 at a time
+        const int base0 = lo + kAttTile * warp;
+        const int nt = hi > base0 ? (hi - base0 + kAttUnit - 1) / kAttUnit : 0;
+        // this lane's token of tile i: its row in the cache, or -1
+        const auto row_of = [&](int i) -> int64_t {
+            const int pos = base0 + i * kAttUnit + lane;
+            if (i >= nt || pos >= hi) return -1;
+            const int64_t row = kv_row(A.cache, A.batch, seq, pos, head);
+            if (row < 0) atomicOr(A.status, STATUS_INDEX);
+            return row;
+        };
+        const auto issue = [&](int i, int64_t row) {
+            if (i < nt) {
+                const uint32_t st = ring_s + (i % RING) * Sh::STAGE;
+                constexpr int CPR = D / 32;                     // 16-byte chunks per code row
+#pragma unroll
+                for (int k = 0; k < CPR; ++k) {
+                    const int t = (k * 32 + lane) / CPR, ch = (k * 32 + lane) % CPR;
+                    const int64_t rw = __shfl_sync(0xffffffffu, row, t);
+                    const int64_t off = rw < 0 ? 0 : rw * (D / 2) + ch * 16;
+                    const uint32_t d = st + code_off<D>(t, ch);
+                    cp16(d, A.cache.k_codes + off, rw >= 0);
+                    cp16(d + Sh::CB, A.cache.v_codes + off, rw >= 0);
+                }
+                // scales: chunks of 16 bytes, 16 / SB consecutive tokens of one page
+                constexpr int CH = kAttTile * Sh::SB / 16;
+#pragma unroll
+                for (int k = 0; k < (2 * CH + 31) / 32; ++k) {
+                    const int x = k * 32 + lane, ch = x % CH;
+                    const int64_t rw = __shfl_sync(0xffffffffu, row, ch * 16 / Sh::SB);
+                    if (x < 2 * CH)
+                        cp16(st + 2 * Sh::CB + (x / CH) * Sh::TB + ch * 16,
+                             reinterpret_cast<const uint8_t *>(x < CH ? A.cache.k_scales : A.cache.v_scales) +
+                                 (rw < 0 ? 0 : rw * Sh::SB),
+                             rw >= 0);
+                }
+            }
+            cp_commit();
+        };
+        int64_t row_next = row_of(0);
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) {
+            const int64_t row = row_next;
+            row_next = row_of(i + 1);
+            issue(i, row);
+        }
+        for (int it = 0; it < nt; ++it) {
+            {
+                const int64_t row = row_next;
+                row_next = row_of(it + RING);
+                issue(it + RING - 1, row);
+            }
+            cp_wait<RING - 1>();
+            __syncwarp();
+            uint8_t *const st = ring + (it % RING) * Sh::STAGE;
+            const uint32_t st_s = ring_s + (it % RING) * Sh::STAGE;
+            uint8_t *const ks = st + 2 * Sh::CB, *const vs = ks + Sh::TB;
+            const int base = base0 + it * kAttUnit;
+            // value scales of tokens that no row sees count as zero
+            if (base + kAttTile > hi) {
+                if (base + lane >= hi) Sw::zero(vs + lane * Sh::SB);
+                __syncwarp();
+            }
+            int ev;                                             // exponent of the tile's largest value scale
+            {
+                Sw v;
+                v.load(vs + lane * Sh::SB);
+                ev = max(__reduce_max_sync(0xffffffffu, v.template top<GS>()), -90);
+            }
+            // ---- scores
+            float sc[2][NB][4];
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb) {
+                Sw k0, k8;
+                k0.load(ks + (mb * 16 + r) * Sh::SB);
+                k8.load(ks + (mb * 16 + r + 8) * Sh::SB);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[mb][nb][k] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NJ; j += 2) {
+                    uint32_t w[4];
+                    ldsm4<false>(w, st_s + code_off<D>(mb * 16 + lm_t, j + lm_c));
+                    float acc[NB][4];
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        uint32_t x[4], y[4];
+                        if constexpr (CODES == CODES_INT4) {
+                            int4_halves(w[2 * jj], x);
+                            int4_halves(w[2 * jj + 1], y);
+                        } else {
+                            e2m1_bytes(w[2 * jj], x);
+                            e2m1_bytes(w[2 * jj + 1], y);
+                        }
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            const uint32_t(&q)[4] = qf[nb][j + jj];
+                            if constexpr (G == 16) {
+                                // lanes 0, 1 of a quad hold the first group's channels, 2, 3 the second's
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    const bool on = (c >> 1) == half;
+                                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                    mma_f16(d, x[0], y[0], x[1], y[1], on ? q[0] : 0u, on ? q[1] : 0u);
+                                    mma_f16(d, x[2], y[2], x[3], y[3], on ? q[2] : 0u, on ? q[3] : 0u);
+                                    const int g = 2 * (j + jj) + half;
+                                    const float s0 = k0.template get<GS>(g), s8 = k8.template get<GS>(g);
+                                    sc[mb][nb][0] = fmaf(d[0], s0, sc[mb][nb][0]);
+                                    sc[mb][nb][1] = fmaf(d[1], s0, sc[mb][nb][1]);
+                                    sc[mb][nb][2] = fmaf(d[2], s8, sc[mb][nb][2]);
+                                    sc[mb][nb][3] = fmaf(d[3], s8, sc[mb][nb][3]);
+                                }
+                            } else {
+                                if (G == 32 || jj == 0) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) acc[nb][k] = 0.0f;
+                                }
+                                mma_f16(acc[nb], x[0], y[0], x[1], y[1], q[0], q[1]);
+                                mma_f16(acc[nb], x[2], y[2], x[3], y[3], q[2], q[3]);
+                                if (G == 32 || jj == 1) {
+                                    const int g = (j + jj) * 32 / G;
+                                    const float s0 = k0.template get<GS>(g), s8 = k8.template get<GS>(g);
+                                    sc[mb][nb][0] = fmaf(acc[nb][0], s0, sc[mb][nb][0]);
+                                    sc[mb][nb][1] = fmaf(acc[nb][1], s0, sc[mb][nb][1]);
+                                    sc[mb][nb][2] = fmaf(acc[nb][2], s8, sc[mb][nb][2]);
+                                    sc[mb][nb][3] = fmaf(acc[nb][3], s8, sc[mb][nb][3]);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            // ---- softmax: the running maximum carries the exponent of the
+            // tile's value scales, so that p s stays below 2^15 (m is at
+            // least the largest score + exponent - 14 of every tile)
+            const bool cut = base + kAttTile > lim_min;
+            bool moved = false;
+            float alpha[NB][2], mu[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float t = -INFINITY;
+#pragma unroll
+                    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float &x = sc[mb][nb][2 * k + h];
+                            x *= fac[nb][h];
+                            if (cut && base + mb * 16 + 8 * k + r >= lim[nb][h]) x = -INFINITY;
+                            t = max_nan(t, x);
+                        }
+                    t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    alpha[nb][h] = t;
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float old = m[nb][h];
+                    const float now = max_nan(old, alpha[nb][h] + (float)(ev - 14));
+                    m[nb][h] = now;
+                    mu[nb][h] = now == -INFINITY ? 0.0f : now;
+                    alpha[nb][h] = ex2(old - mu[nb][h]);
+                    moved |= now != old;
+                }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    l[nb][0] *= alpha[nb][0];
+                    l[nb][1] *= alpha[nb][1];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[nb][j][k >> 2][k & 3] *= alpha[nb][k & 1];
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float p = ex2(sc[mb][nb][k] - mu[nb][k & 1]);
+                        sc[mb][nb][k] = p;
+                        l[nb][k & 1] += p;
+                    }
+            // ---- values
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb) {
+                Sw v0, v8;
+                v0.load(vs + (mb * 16 + r) * Sh::SB);
+                v8.load(vs + (mb * 16 + r + 8) * Sh::SB);
+                uint32_t p0[NB], p1[NB], p2[NB], p3[NB];        // B operands of the group(s) at hand
+                const auto probs = [&](int g, uint32_t(&b0)[NB], uint32_t(&b1)[NB]) {
+                    const float s0 = v0.template get<GS>(g), s8 = v8.template get<GS>(g);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        b0[nb] = movm(f16x2_rn(sc[mb][nb][0] * s0, sc[mb][nb][1] * s0));
+                        b1[nb] = movm(f16x2_rn(sc[mb][nb][2] * s8, sc[mb][nb][3] * s8));
+                    }
+                };
+#pragma unroll
+                for (int j = 0; j < NJ; j += 2) {
+                    uint32_t w[4];
+                    ldsm4<true>(w, st_s + Sh::CB + code_off<D>(mb * 16 + lm_t, j + lm_c));
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        uint32_t wa = w[2 * jj], wb = w[2 * jj + 1];
+                        if constexpr (G == 16) {
+                            // a lane of the lower four rows holds nibbles of the first
+                            // group, one of the upper four of the second; half of them
+                            // change places, so that nibbles 0, 1 are the first group's
+                            // and 2, 3 the second's in every lane
+                            const bool up = (r & 4) != 0;
+                            const uint32_t give = prmt(wa, wb, up ? 0x6420u : 0x7531u);
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 16);
+                            wa = prmt(wa, got, up ? 0x3514u : 0x5240u);
+                            wb = prmt(wb, got, up ? 0x3716u : 0x7260u);
+                            probs(2 * (j + jj), p0, p1);
+                            probs(2 * (j + jj) + 1, p2, p3);
+                        } else if (G == 32 || jj == 0) {
+                            probs((j + jj) * 32 / G, p0, p1);
+                        }
+                        uint32_t x[4], y[4];
+                        nibble_pairs<CODES>(wa, x);
+                        nibble_pairs<CODES>(wb, y);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma_f16(o[nb][j + jj][0], x[0], x[1], y[0], y[1], p0[nb], p1[nb]);
+                            if constexpr (G == 16)
+                                mma_f16(o[nb][j + jj][1], x[2], x[3], y[2], y[3], p2[nb], p3[nb]);
+                            else
+                                mma_f16(o[nb][j + jj][1], x[2], x[3], y[2], y[3], p0[nb], p1[nb]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        cp_wait<0>();
+        __syncthreads();                                        // the ring becomes the joining buffer
+
+        // ---- join the warps
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float t = l[nb][h];
+                t += __shfl_xor_sync(0xffffffffu, t, 4);
+                t += __shfl_xor_sync(0xffffffffu, t, 8);
+                t += __shfl_xor_sync(0xffffffffu, t, 16);
+                const int row = 8 * nb + 2 * c + h;
+                if (r == 0) join_ml[warp * ROWS + row] = make_float2(m[nb][h], t);
+                float *const dst = join + (warp * ROWS + row) * Sh::OST;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if constexpr (G == 16) {
+#pragma unroll
+                        for (int blk = 0; blk < 2; ++blk)
+                            *reinterpret_cast<float2 *>(dst + 32 * j + 16 * blk + 4 * (r & 3) + 2 * (r >> 2)) =
+                                make_float2(o[nb][j][blk][h], o[nb][j][blk][2 + h]);
+                    } else {
+                        *reinterpret_cast<float4 *>(dst + 32 * j + 4 * r) =
+                            make_float4(o[nb][j][0][h], o[nb][j][0][2 + h], o[nb][j][1][h], o[nb][j][1][2 + h]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == sp.kvt;
+        const int slot = 2 * me + (t0 == 0 ? 1 : 0);
+        for (int x = tid; x < rows * (D / 4); x += kAttThreads) {
+            const int row = x / (D / 4), d = 4 * (x % (D / 4));
+            float mx = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kAttWarps; ++w) mx = max_nan(mx, join_ml[w * ROWS + row].x);
+            const float base = mx == -INFINITY ? 0.0f : mx;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttWarps; ++w) {
+                const float2 ml = join_ml[w * ROWS + row];
+                const float f = ex2(ml.x - base);
+                const float4 v = *reinterpret_cast<const float4 *>(join + (w * ROWS + row) * Sh::OST + d);
+                sum = fmaf(ml.y, f, sum);
+                acc.x = fmaf(v.x, f, acc.x);
+                acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z);
+                acc.w = fmaf(v.w, f, acc.w);
+            }
+            if (whole) {
+                const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+                const int rr = row0 + row, tok = rr / A.group;
+                uint2 v;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(acc.y * inv), "f"(acc.x * inv));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(acc.w * inv), "f"(acc.z * inv));
+                *reinterpret_cast<uint2 *>(A.out + (s.s0 + tok) * A.out_token +
+                                           (int64_t)(head * A.group + rr - tok * A.group) * A.out_head + d) = v;
+            } else {
+                *reinterpret_cast<float4 *>(A.part + ((int64_t)slot * ROWS + row) * D + d) = acc;
+                if (d == 0) A.part_ml[slot * ROWS + row] = make_float2(mx, sum);
+            }
+        }
+        if (!whole && t0 == 0 && tid == 0) {
+            AttMeta mt;
+            mt.end = first + (long long)(seg + 1) * sp.kvt;
+            mt.units = units;
+            mt.seq = seq;
+            mt.seg = seg;
+            A.meta[me] = mt;
+        }
+        __syncthreads();
+        u += t1 - t0;
+    }
+}
+
+// Joins the pieces of the segments that were cut: CTA (i, row) takes the one
+// that starts in share i.  Four warps take every fourth piece each; their
+// sums are added in a fixed order.
+template <int D, int NB>
+__global__ void __launch_bounds__(128)
+attend_join_kernel(const AttArgs A, int n) {
+    grid_dependency_begin();
+    constexpr int ROWS = 8 * NB;
+    __shared__ float4 s_acc[4][D / 4];
+    __shared__ float s_sum[4];
+    const AttMeta mt = A.meta[blockIdx.x];
+    if (mt.seq < 0) return;
+    const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, mt.seq);
+    const AttSpan sp = att_span<ROWS>(s, A.group, A.cache.heads);
+    const int head = mt.seg / sp.qt, rr = (mt.seg - head * sp.qt) * ROWS + row;
+    if (rr >= s.n * A.group) return;
+    // shares i, i + 1, ..., last hold pieces (empty shares hold none)
+    const int i0 = blockIdx.x;
+    const int last = (int)min((long long)n - 1, (mt.end * n - 1) / mt.units);
+    const auto piece = [&](int i) {             // slot, or -1
+        if (mt.units < n && i > i0 && mt.units * i / n >= mt.units * (i + 1) / n) return -1;
+        return 2 * i + (i == i0 ? 1 : 0);
+    };
+    float mx = -INFINITY;
+    for (int i = i0 + lane; i <= last; i += 32) {
+        const int k = piece(i);
+        if (k >= 0) mx = max_nan(mx, A.part_ml[k * ROWS + row].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int i = i0 + warp; i <= last; i += 4) {
+        const int k = piece(i);
+        if (k < 0) continue;
+        const float2 ml = A.part_ml[k * ROWS + row];
+        const float f = ex2(ml.x - base);
+        sum = fmaf(ml.y, f, sum);
+        if (4 * lane < D) {
+            const float4 v = *reinterpret_cast<const float4 *>(A.part + ((int64_t)k * ROWS + row) * D + 4 * lane);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+        }
+    }
+    if (4 * lane < D) s_acc[warp][lane] = acc;
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (warp != 0 || 4 * lane >= D) return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+        const float4 v = s_acc[w][lane];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        sum += s_sum[w];
+    }
+    const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+    const int tok = rr / A.group;
+    uint2 v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(acc.y * inv), "f"(acc.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(acc.w * inv), "f"(acc.z * inv));
+    *reinterpret_cast<uint2 *>(A.out + (s.s0 + tok) * A.out_token +
+                               (int64_t)(head * A.group + rr - tok * A.group) * A.out_head + 4 * lane) = v;
+}
+
+// ---- launch
+
+inline AttArgs att_args(const AttendLaunch &L, int rows) {
+    AttArgs A;
+    A.q = static_cast<const uint16_t *>(L.q);
+    A.q_token = L.q_token;
+    A.q_head = L.q_head;
+    A.out = static_cast<uint16_t *>(L.out);
+    A.out_token = L.out_token;
+    A.out_head = L.out_head;
+    A.tokens = L.tokens;
+    A.group = L.q_heads / L.cache.heads;
+    A.scale_log2 = L.scale * 1.44269504088896341f;
+    A.causal = L.causal;
+    A.cache = L.cache;
+    A.batch = L.batch;
+    uint8_t *w = static_cast<uint8_t *>(L.workspace);
+    A.part = reinterpret_cast<float *>(w);
+    w += (size_t)2 * kAttCtas * rows * L.cache.head_dim * sizeof(float);
+    A.part_ml = reinterpret_cast<float2 *>(w);
+    w += (size_t)2 * kAttCtas * rows * sizeof(float2);
+    A.meta = reinterpret_cast<AttMeta *>(w);
+    A.status = L.status;
+    return A;
+}
+
+template <int CODES, int GS, int G, int D, int NB>
+cudaError_t launch_attend_split(AttendLaunch &L) {
+    using Sh = AttShape<CODES, GS, G, D, NB>;
+    const AttArgs A = att_args(L, Sh::ROWS);
+    const auto kern = attend_split_kernel<CODES, GS, G, D, NB>;
+    static std::atomic<bool> done[64];
+    cudaError_t e = smem_opt_in(kern, Sh::BYTES, done);
+    if (e != cudaSuccess) return e;
+    e = launch_k(kern, dim3(kAttCtas), dim3(kAttThreads), Sh::BYTES, L.stream, A);
+    if (e != cudaSuccess) return e;
+    L.launches = 2;
+    return launch_k(attend_join_kernel<D, NB>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
+}
+
+template <int CODES, int GS, int G, int D>
+cudaError_t launch_attend_d(AttendLaunch &L) {
+    const int64_t rows = L.tokens * (L.q_heads / L.cache.heads);
+    if (rows <= 8 * (int64_t)L.batch.seqs) return launch_attend_split<CODES, GS, G, D, 1>(L);
+    return launch_attend_split<CODES, GS, G, D, 2>(L);
+}
+
+template <int CODES, int GS>
+cudaError_t launch_attend_fmt(AttendLaunch &L) {
+#define DQ_ATT(GG, DD) \
+    if (L.group == GG && L.cache.head_dim == DD) return launch_attend_d<CODES, GS, GG, DD>(L);
+    DQ_ATT(16, 64) DQ_ATT(32, 64) DQ_ATT(64, 64) DQ_ATT(16, 128) DQ_ATT(32, 128) DQ_ATT(64, 128)
+#undef DQ_ATT
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace dq

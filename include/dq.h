@@ -67,7 +67,9 @@ typedef enum dq_status {
     DQ_ERR_NOT_IMPLEMENTED = -8,
     DQ_ERR_ALIGN = -9,          /* a pointer misses its alignment */
     DQ_ERR_SCRATCH = -10,       /* matrix needs more than the built-in scratch buffer */
-    DQ_ERR_TIMEOUT = -11        /* (device flag) a bounded wait in a kernel ran out */
+    DQ_ERR_TIMEOUT = -11,       /* (device flag) a bounded wait in a kernel ran out */
+    DQ_ERR_INDEX = -12          /* (device flag) a sequence start, length or page of a
+                                   dq_kv_batch out of range (dq_serving.h) */
 } dq_status;
 
 /* Code (element) types: the pages' INT4 and E2M1 codebooks, and the other
@@ -358,8 +360,9 @@ DQ_API dq_status dq_test_stall_next_gemm(void);
 /* Synchronise `stream`, read and clear the device flags raised by earlier
  * calls on this device: DQ_ERR_NONFINITE if an input held NaN/Inf (or
  * scaling it by the outer scales left the float32 range),
+ * DQ_ERR_INDEX if a key/value batch named a place out of range,
  * DQ_ERR_RANGE if an outer scale was clamped at its set's bound, DQ_OK
- * otherwise (NONFINITE wins when both are set).  The flags are one word per
+ * otherwise (the first of these wins when several are set).  The flags are one word per
  * device shared by all streams. */
 DQ_API dq_status dq_last_device_status(dq_stream stream);
 
