@@ -13,8 +13,10 @@ kv_lens[s] positions, position p of it in page block_table[s, p // page_size].
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
-from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
+import struct
+from ctypes import byref, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
 
@@ -36,6 +38,16 @@ class dq_kv_batch(ctypes.Structure):
                 ("seqs", c_int32), ("max_pages", c_int32), ("table_stride", c_int64)]
 
 
+# The same two structures as bytes: packing them takes a third of the time of
+# filling a ctypes.Structure, and a call's Python side is what a small call
+# costs (a single token's kernels run for 2 to 10 us).
+_pack_cache = struct.Struct("PPPPqiii4x").pack
+_pack_batch = struct.Struct("PPPiiq").pack
+assert struct.calcsize("PPPPqiii4x") == ctypes.sizeof(dq_kv_cache)
+assert struct.calcsize("PPPiiq") == ctypes.sizeof(dq_kv_batch)
+
+_bf16 = torch.bfloat16
+_new = torch.empty_strided            # (half the time of torch.empty)
 _fns = None
 
 
@@ -59,61 +71,48 @@ def _lib():
     return _fns
 
 
-class _On:
-    """Device and stream of a call: the tensors' device is made current for
-    the launch, and the stream defaults to that device's current one."""
-
-    def __init__(self, device, stream):
-        self.index = device.index
-        self.stream = stream
-        self.back = None
-
-    def __enter__(self):
-        if self.index != torch.cuda.current_device():
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
-        s = self.stream
-        return (torch.cuda.current_stream() if s is None else s).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
-
-
 def _check(status, where):
-    if status != 0:
-        from . import DqError
-        raise DqError(status, where)
+    from . import DqError
+    raise DqError(status, where)
 
 
-def _device(first, *others):
-    """The one CUDA device of the tensors (None skipped)."""
-    if not first.is_cuda:
+def _device(tensors):
+    """Index of the one CUDA device of the tensors (None skipped)."""
+    d = tensors[0].get_device()
+    if d < 0:
         raise ValueError("tensors must be CUDA tensors")
-    d = first.device
-    for t in others:
-        if t is not None and t.device != d:
+    for t in tensors:
+        if t is not None and t.get_device() != d:
             raise ValueError("tensors must be on one CUDA device")
     return d
 
 
-def _bf16(t, name, dims):
-    if t.dtype != torch.bfloat16:
+def _call(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current; the stream defaults
+    to that device's current one."""
+    back = torch._C._cuda_getDevice()
+    if back == device:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
+                  else stream.cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
+                  else stream.cuda_stream)
+
+
+def _rows(t, name):
+    """(shape, element strides of the leading dimensions) of a bf16 array
+    whose last dimension is contiguous; a dimension of one element takes the
+    stride of a contiguous tensor (torch leaves it arbitrary)."""
+    if t.dtype is not _bf16:
         raise TypeError(f"{name} is bfloat16")
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name}: {dims} dimensions, the last one contiguous")
-    return t
-
-
-def _strides(t):
-    """Element strides of the leading dimensions; a dimension of one element
-    takes the stride of a contiguous tensor (torch leaves it arbitrary)."""
-    out = []
-    inner = t.shape[-1]
-    for i in range(t.dim() - 2, -1, -1):
-        out.append(inner if t.shape[i] <= 1 else t.stride(i))
-        inner *= max(t.shape[i], 1)
-    return out[::-1]
+    shape, st = t.shape, t.stride()
+    if len(shape) == 2:
+        if st[1] == 1 or shape[1] <= 1:
+            return shape, (st[0] if shape[0] > 1 else shape[1],)
+    elif len(shape) == 3 and (st[2] == 1 or shape[2] <= 1):
+        head = st[1] if shape[1] > 1 else shape[2]
+        return shape, (st[0] if shape[0] > 1 else max(head * shape[1], shape[2]), head)
+    raise ValueError(f"{name}: the last dimension is contiguous")
 
 
 def add_rmsnorm_quant(x, weight, fmt, residual=None, b=None, eps=1e-5, codes=None, gscales=None,
@@ -127,34 +126,56 @@ def add_rmsnorm_quant(x, weight, fmt, residual=None, b=None, eps=1e-5, codes=Non
     none is passed; pass ``residual`` itself to update it in place) rounded
     to bf16; the norm uses the unrounded float32 sum.  weight: [K] float32 or
     bf16; b: [K] float32 (the solver's inverse column scales) or None."""
-    from . import _dtype_code, _outputs
-    dev = _device(x, weight, residual, b, codes, gscales, residual_out)
-    _bf16(x, "x", 2)
-    tokens, K = x.shape
+    dev = _device((x, weight, residual, b, codes, gscales, residual_out))
+    (tokens, K), (xs,) = _rows(x, "x")
     if weight.shape != (K,) or not weight.is_contiguous():
         raise ValueError("weight: [K], contiguous")
-    if b is not None and (b.dtype != torch.float32 or b.shape != (K,) or not b.is_contiguous()):
+    wd = weight.dtype
+    if wd is not _bf16 and wd is not torch.float32:
+        raise TypeError("weight is float32 or bfloat16")
+    if b is not None and (b.dtype is not torch.float32 or b.shape != (K,) or not b.is_contiguous()):
         raise ValueError("b: float32 [K], contiguous")
-    if residual is not None and _bf16(residual, "residual", 2).shape != x.shape:
-        raise ValueError("residual: the shape of x")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(tokens, K, dtype=torch.bfloat16, device=dev)
-    if residual_out is not None and _bf16(residual_out, "residual_out", 2).shape != x.shape:
-        raise ValueError("residual_out: the shape of x")
+    rp = op = None
+    rs = os = 0
+    if residual is not None:
+        shape, (rs,) = _rows(residual, "residual")
+        if shape != (tokens, K):
+            raise ValueError("residual: the shape of x")
+        rp = residual.data_ptr()
+        if residual_out is None:
+            residual_out = _new((tokens, K), (K, 1), dtype=_bf16, device=x.device)
+    if residual_out is not None:
+        shape, (os,) = _rows(residual_out, "residual_out")
+        if shape != (tokens, K):
+            raise ValueError("residual_out: the shape of x")
+        op = residual_out.data_ptr()
     if codes is None or gscales is None:
-        codes, gscales = _outputs(tokens, K, fmt, dev, codes, gscales)
-    for t, name in ((codes, "codes"), (gscales, "gscales")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous")
-    res, ro = residual, residual_out
-    with _On(dev, stream) as st:
-        _check(_lib().dq_add_rmsnorm_quant(
-            x.data_ptr(), _strides(x)[0], None if res is None else res.data_ptr(),
-            0 if res is None else _strides(res)[0], weight.data_ptr(), _dtype_code(weight),
-            None if b is None else b.data_ptr(), eps, tokens, K, ctypes.byref(fmt),
-            None if ro is None else ro.data_ptr(), 0 if ro is None else _strides(ro)[0],
-            codes.data_ptr(), gscales.data_ptr(), st), "dq_add_rmsnorm_quant")
+        codes, gscales = _outputs(tokens, K, fmt, x.device, codes, gscales)
+    if not (codes.is_contiguous() and gscales.is_contiguous()):
+        raise ValueError("codes and gscales: contiguous")
+    status = _call(dev, stream, _lib().dq_add_rmsnorm_quant, x.data_ptr(), xs, rp, rs,
+                   weight.data_ptr(), 1 if wd is _bf16 else 0, None if b is None else b.data_ptr(), eps,
+                   tokens, K, byref(fmt), op, os, codes.data_ptr(), gscales.data_ptr())
+    if status:
+        _check(status, "dq_add_rmsnorm_quant")
     return codes, gscales, residual_out
+
+
+_BITS = (4, 4, 8, 8, 8, 6, 6)           # of a code, by DQ_CODES_*
+
+
+def _outputs(tokens, K, fmt, device, codes, gscales):
+    if not 0 <= fmt.codes < 7 or fmt.group <= 0 or K % fmt.group:
+        from . import DqError
+        raise DqError(-2 if 0 <= fmt.codes < 7 and fmt.group > 0 else -3, "dq_add_rmsnorm_quant")
+    if codes is None:
+        n = K * _BITS[fmt.codes] // 8
+        codes = _new((tokens, n), (n, 1), dtype=torch.uint8, device=device)
+    if gscales is None:
+        n = K // fmt.group
+        gscales = _new((tokens, n), (n, 1), dtype=torch.int16 if fmt.group_scale == 0 else torch.uint8,
+                       device=device)
+    return codes, gscales
 
 
 def kv_cache(pages, page_size, heads, head_dim, fmt, device="cuda"):
@@ -167,49 +188,51 @@ def kv_cache(pages, page_size, heads, head_dim, fmt, device="cuda"):
 
 
 def _cache(cache, fmt):
+    """(packed structure, heads, head_dim) of a cache."""
     kc, ks, vc, vs = cache
-    pages, heads, page_size, half = kc.shape
-    if vc.shape != kc.shape or kc.dtype != torch.uint8 or vc.dtype != torch.uint8:
+    shape = kc.shape
+    pages, heads, page_size, half = shape
+    if vc.shape != shape or kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8:
         raise ValueError("cache codes: uint8 [pages, heads, page_size, head_dim / 2]")
     want = (pages, heads, page_size, 2 * half // max(fmt.group, 1))
-    bits = 2 if fmt.group_scale == 0 else 1
-    for s in (ks, vs):
-        if tuple(s.shape) != want or s.element_size() != bits:
-            raise ValueError(f"cache scales: {list(want)} of {8 * bits} bits")
-    for t in cache:
-        if not t.is_contiguous():
-            raise ValueError("cache tensors: contiguous")
-    return dq_kv_cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page_size,
-                       heads, 2 * half)
+    size = 2 if fmt.group_scale == 0 else 1
+    if ks.shape != want or vs.shape != want or ks.element_size() != size or vs.element_size() != size:
+        raise ValueError(f"cache scales: {list(want)} of {8 * size} bits")
+    if not (kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("cache tensors: contiguous")
+    return (_pack_cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page_size,
+                        heads, 2 * half), heads, 2 * half)
+
+
+_i32 = torch.int32
 
 
 def _batch(starts, kv_lens, block_table):
-    seqs = kv_lens.shape[0]
-    if starts.dim() != 1 or starts.shape[0] != seqs + 1 or kv_lens.dim() != 1 or \
-            block_table.dim() != 2 or block_table.shape[0] != seqs:
+    """(packed structure, sequences) of a batch."""
+    ns, nl, nt = starts.shape, kv_lens.shape, block_table.shape
+    if len(nl) != 1 or len(ns) != 1 or len(nt) != 2 or ns[0] != nl[0] + 1 or nt[0] != nl[0]:
         raise ValueError("starts [seqs + 1], kv_lens [seqs], block_table [seqs, pages]")
-    for t in (starts, kv_lens, block_table):
-        if t.dtype != torch.int32:
-            raise TypeError("starts, kv_lens and block_table are int32")
-    if not starts.is_contiguous() or not kv_lens.is_contiguous() or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    if starts.dtype is not _i32 or kv_lens.dtype is not _i32 or block_table.dtype is not _i32:
+        raise TypeError("starts, kv_lens and block_table are int32")
+    seqs, cols = nt
+    st = block_table.stride()
+    if not (starts.is_contiguous() and kv_lens.is_contiguous()) or (cols > 1 and st[1] != 1):
         raise ValueError("starts, kv_lens and the rows of block_table: contiguous")
-    cols = block_table.shape[1]
-    return dq_kv_batch(starts.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), seqs, cols,
-                       cols if seqs <= 1 else block_table.stride(0))
+    return (_pack_batch(starts.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), seqs, cols,
+                        cols if seqs <= 1 else st[0]), seqs)
 
 
 def _copy(fn, name, k, v, cache, starts, kv_lens, block_table, fmt, stream):
-    c, b = _cache(cache, fmt), _batch(starts, kv_lens, block_table)
-    for t, what in ((k, "k"), (v, "v")):
-        if _bf16(t, what, 3).shape[1:] != (c.heads, c.head_dim) or t.shape[0] != k.shape[0]:
-            raise ValueError(f"{what}: [tokens, heads, head_dim] of the cache")
-    dev = _device(k, v, *cache, starts, kv_lens, block_table)
-    kt, kh = _strides(k)
-    vt, vh = _strides(v)
-    with _On(dev, stream) as st:
-        _check(fn(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, k.shape[0], ctypes.addressof(c),
-                  ctypes.addressof(b), ctypes.byref(fmt), st), name)
+    c, heads, dim = _cache(cache, fmt)
+    b, _ = _batch(starts, kv_lens, block_table)
+    ks, (kt, kh) = _rows(k, "k")
+    vs, (vt, vh) = _rows(v, "v")
+    if len(ks) != 3 or vs != ks or ks[1] != heads or ks[2] != dim:
+        raise ValueError("k and v: [tokens, heads, head_dim] of the cache")
+    dev = _device((k, v, *cache, starts, kv_lens, block_table))
+    status = _call(dev, stream, fn, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ks[0], c, b, byref(fmt))
+    if status:
+        _check(status, name)
 
 
 def kv_append(k, v, cache, starts, kv_lens, block_table, fmt, stream=None):
@@ -222,23 +245,26 @@ def kv_read(cache, starts, kv_lens, block_table, fmt, tokens, k=None, v=None, st
     """The values the cache holds for the batch's new tokens: (k, v) bf16
     [tokens, heads, head_dim].  Rows that belong to no sequence are left as
     they are (undefined in tensors allocated here)."""
-    pages, heads, page_size, half = cache[0].shape
-    dev = cache[0].device
+    _, heads, _, half = cache[0].shape
     if k is None:
-        k = torch.empty(tokens, heads, 2 * half, dtype=torch.bfloat16, device=dev)
+        k = _new((tokens, heads, 2 * half), (2 * heads * half, 2 * half, 1), dtype=_bf16,
+                 device=cache[0].device)
     if v is None:
-        v = torch.empty(tokens, heads, 2 * half, dtype=torch.bfloat16, device=dev)
+        v = _new((tokens, heads, 2 * half), (2 * heads * half, 2 * half, 1), dtype=_bf16,
+                 device=cache[0].device)
     if k.shape[0] != tokens:
         raise ValueError("k: [tokens, heads, head_dim]")
     _copy(_lib().dq_kv_read, "dq_kv_read", k, v, cache, starts, kv_lens, block_table, fmt, stream)
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def kv_attention_workspace(tokens, q_heads, heads, head_dim, seqs) -> int:
     """Bytes of workspace ``kv_attention`` needs."""
     out = c_size_t(0)
-    _check(_lib().dq_kv_attention_workspace(tokens, q_heads, heads, head_dim, seqs,
-                                            ctypes.addressof(out)), "dq_kv_attention_workspace")
+    status = _lib().dq_kv_attention_workspace(tokens, q_heads, heads, head_dim, seqs, byref(out))
+    if status:
+        _check(status, "dq_kv_attention_workspace")
     return out.value
 
 
@@ -254,26 +280,28 @@ def kv_attention(q, cache, starts, kv_lens, block_table, fmt, scale=None, causal
     in a tensor allocated here).  ws: a uint8 tensor of
     ``kv_attention_workspace`` bytes (allocated when None); calls that may
     overlap on the device need one each."""
-    c, b = _cache(cache, fmt), _batch(starts, kv_lens, block_table)
-    if _bf16(q, "q", 3).shape[2] != c.head_dim:
+    c, heads, dim = _cache(cache, fmt)
+    b, seqs = _batch(starts, kv_lens, block_table)
+    shape, (qt, qh) = _rows(q, "q")
+    if len(shape) != 3 or shape[2] != dim:
         raise ValueError("q: [tokens, q_heads, head_dim] of the cache")
-    dev = _device(q, *cache, starts, kv_lens, block_table, out, ws)
-    tokens, q_heads, dim = q.shape
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(tokens, q_heads, dim, dtype=torch.bfloat16, device=dev)
-        elif _bf16(out, "out", 3).shape != q.shape:
+    dev = _device((q, *cache, starts, kv_lens, block_table, out, ws))
+    tokens, q_heads, _ = shape
+    if out is None:
+        ot, oh = q_heads * dim, dim
+        out = _new(shape, (ot, oh, 1), dtype=_bf16, device=q.device)
+    else:
+        so, (ot, oh) = _rows(out, "out")
+        if so != shape:
             raise ValueError("out: the shape of q")
-        if ws is None:
-            ws = torch.empty(kv_attention_workspace(tokens, q_heads, c.heads, dim, b.seqs),
-                             dtype=torch.uint8, device=dev)
-            if stream is not None:
-                ws.record_stream(stream)
-        qt, qh = _strides(q)
-        ot, oh = _strides(out)
-        _check(_lib().dq_kv_attention(
-            q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, tokens, q_heads,
-            1.0 / math.sqrt(dim) if scale is None else scale, 1 if causal else 0,
-            ctypes.addressof(c), ctypes.addressof(b), ctypes.byref(fmt), ws.data_ptr(), ws.numel(),
-            st), "dq_kv_attention")
+    if ws is None:
+        ws = _new((kv_attention_workspace(tokens, q_heads, heads, dim, seqs),), (1,), dtype=torch.uint8,
+                  device=q.device)
+        if stream is not None:
+            ws.record_stream(stream)
+    status = _call(dev, stream, _lib().dq_kv_attention, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                   tokens, q_heads, 1.0 / math.sqrt(dim) if scale is None else scale, 1 if causal else 0,
+                   c, b, byref(fmt), ws.data_ptr(), ws.nbytes)
+    if status:
+        _check(status, "dq_kv_attention")
     return out
