@@ -880,20 +880,4 @@ cudaError_t launch_attend_split(AttendLaunch &L) {
     return launch_k(attend_join_kernel<D, NB>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
 }
 
-template <int CODES, int GS, int G, int D>
-cudaError_t launch_attend_d(AttendLaunch &L) {
-    const int64_t rows = L.tokens * (L.q_heads / L.cache.heads);
-    if (rows <= 8 * (int64_t)L.batch.seqs) return launch_attend_split<CODES, GS, G, D, 1>(L);
-    return launch_attend_split<CODES, GS, G, D, 2>(L);
-}
-
-template <int CODES, int GS>
-cudaError_t launch_attend_fmt(AttendLaunch &L) {
-#define DQ_ATT(GG, DD) \
-    if (L.group == GG && L.cache.head_dim == DD) return launch_attend_d<CODES, GS, GG, DD>(L);
-    DQ_ATT(16, 64) DQ_ATT(32, 64) DQ_ATT(64, 64) DQ_ATT(16, 128) DQ_ATT(32, 128) DQ_ATT(64, 128)
-#undef DQ_ATT
-    return cudaErrorInvalidValue;
-}
-
 }  // namespace dq

@@ -1,4 +1,4 @@
-#include "dq_attend.cuh"
+#include "dq_attend_prompt.cuh"
 
 namespace dq {
 

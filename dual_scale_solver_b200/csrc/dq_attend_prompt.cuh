@@ -1,0 +1,542 @@
+// dq_attend_prompt.cuh — attention of many query rows over the 4-bit cache on
+// the tcgen05 tensor cores.
+//
+// A CTA takes 256 query rows (two tiles of 128; a row is one token and one
+// head of the group, so a group's heads share every code) of one sequence
+// and cache head, and walks the positions in tiles of 128:
+//
+//   S = Q K^T    tcgen05.mma, 128 x 128 x D, both operands fp16 in shared
+//                memory, float32 in TMEM
+//   P = 2^(S f - m)  by the rows' threads (TMEM -> registers -> TMEM, fp16)
+//   O += P V     tcgen05.mma, 128 x D x 128, P from TMEM, V fp16 in shared
+//                memory, float32 in TMEM
+//
+// and the two row tiles take turns, so that one tile's softmax runs while the
+// tensor core works for the other.  The products are bound by the tensor
+// core (4 D flops per pair of row and position, 4096 multiply-adds per clock
+// and SM), closely followed by the exponentials (16 per clock and SM).
+//
+// Codes become fp16 exactly: a code times its group scale has at most 11
+// significant bits, and the scales of a warp's 32 tokens are taken relative
+// to 2^E, E the exponent of the largest of them (what lies 2^-24 or further
+// below is lost to fp16's smallest step).  E of the keys is part of the
+// factor that takes scores to log2 units; E of the values is part of the
+// exponent that P is formed with, and of the running maximum, so that P stays
+// at most 2^15.  The maximum is raised only when it has to grow by more than
+// 2^8 (O is then rescaled in TMEM); P is rounded to fp16 (2^-12 at most), its
+// sum is float32.
+//
+//   warps 0-3, 4-7   softmax of row tile 0, 1: a thread per row; they also
+//                    bring in the row of Q and write the row of the output
+//   warps 8-11       codes -> fp16 tiles: a thread per token, 64 bytes of
+//                    codes in registers while the previous tile is expanded
+//   warp 12          issues the MMAs
+// Every wait is bounded (dq_tc.cuh).
+#pragma once
+
+#include "dq_attend.cuh"
+#include "dq_tc.cuh"
+
+namespace dq {
+
+constexpr int kPromptRows = 256;                 // query rows of a CTA
+constexpr int kPromptTile = 128;                 // positions per step
+constexpr int kPromptThreads = 512;
+constexpr int kPromptK0 = 12;                    // fp16 code x scale: at most 7 * 2^13
+
+template <int D>
+struct __align__(1024) PromptSmem {
+    uint8_t q[2][128 * D * 2];
+    uint8_t k[2][128 * D * 2];
+    uint8_t v[2][128 * D * 2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];     // by row tile
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // by stage
+    uint64_t drained;
+    int ek[8][4], ev[8][4];                      // exponents by tile (mod 8) and 32 tokens
+    uint32_t tmem;
+    int abort;
+};
+
+// Byte of 16-byte chunk c (8 elements) of a row in a tile of 128 rows.
+__device__ __forceinline__ uint32_t prompt_off(int row, int c) {
+    return (uint32_t)((c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+
+struct PromptItem {
+    KvSeq s;
+    int seq, head, row0;
+    int rows[2], nt[2];                          // valid rows and position tiles of each row tile
+    int steps;
+};
+
+// The CTA's items, one per call: a sequence's row tiles go from the last
+// (longest, when causal) to the first, all heads of each; rounds of the grid
+// run forwards and backwards in turn, so that long and short ones pair up.
+struct PromptWalk {
+    int seq = 0, round = 0;
+    long long first = 0;
+    template <class F>
+    __device__ __forceinline__ bool next(const AttArgs &A, PromptItem &it, F bad) {
+        const long long n = gridDim.x;
+        const long long idx = round * n + ((round & 1) ? n - 1 - blockIdx.x : blockIdx.x);
+        ++round;
+        for (; seq < A.batch.seqs; ++seq) {
+            it.s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
+            if (!it.s.ok) bad();
+            const int all = it.s.n * A.group;
+            const int tiles = (all + kPromptRows - 1) / kPromptRows;
+            const long long cnt = (long long)tiles * A.cache.heads;
+            if (idx < first + cnt) {
+                const long long local = idx - first;
+                const int up = (int)(local / A.cache.heads);
+                it.seq = seq;
+                it.head = (int)(local - (long long)up * A.cache.heads);
+                it.row0 = (tiles - 1 - up) * kPromptRows;
+                it.steps = 0;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int r0 = it.row0 + 128 * t;
+                    it.rows[t] = min(max(all - r0, 0), 128);
+                    it.nt[t] = it.rows[t] == 0 ? 0
+                                               : (limit(A, it.s, r0 + it.rows[t] - 1) + kPromptTile - 1) / kPromptTile;
+                    it.steps = max(it.steps, it.nt[t]);
+                }
+                return true;
+            }
+            first += cnt;
+        }
+        return false;
+    }
+    // positions below it are seen by the row
+    __device__ __forceinline__ static int limit(const AttArgs &A, const KvSeq &s, int row) {
+        return A.causal ? min(max(s.len - s.n + row / A.group + 1, 0), s.len) : s.len;
+    }
+};
+
+// One token's codes of one head, and its scales (zeros for row < 0).
+template <int D>
+__device__ __forceinline__ void prompt_codes(uint4 (&c)[D / 32], const uint8_t *codes, int64_t row) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(codes + row * (D / 2));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) c[i] = row >= 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+}
+template <int SB>
+__device__ __forceinline__ void prompt_scales(ScaleWords<SB> &s, const void *scales, int64_t row) {
+    if (row >= 0) {
+        s.load(static_cast<const uint8_t *>(scales) + row * SB);
+    } else {
+#pragma unroll
+        for (int i = 0; i < ScaleWords<SB>::N; ++i) s.w[i] = 0;
+    }
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Expands a token's row into a tile, with scales relative to 2^e; the order of
+// the 8 elements of a chunk is the one the code conversion gives
+// (prompt_order).
+template <int CODES, int GS, int G, int D, int SB>
+__device__ __forceinline__ void prompt_expand(const uint4 (&c)[D / 32], const ScaleWords<SB> &sw, int e,
+                                              uint8_t *tile, int row) {
+    const float down = pow2f(kPromptK0 - e);
+    uint32_t s2[D / G];
+#pragma unroll
+    for (int g = 0; g < D / G; ++g) {
+        const float s = sw.template get<GS>(g) * down;
+        s2[g] = f16x2_rn(s, s);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+            if constexpr (CODES == CODES_INT4) int4_halves(w[k], h);
+            else e2m1_bytes(w[k], h);
+            const uint32_t f = s2[(32 * i + 8 * k) / G];
+            *reinterpret_cast<uint4 *>(tile + prompt_off(row, 4 * i + k)) =
+                make_uint4(hmul2(h[0], f), hmul2(h[1], f), hmul2(h[2], f), hmul2(h[3], f));
+        }
+    }
+}
+
+// Channel (0..7 of a chunk) at place p of a chunk in the tiles.
+template <int CODES>
+__host__ __device__ constexpr int prompt_order(int p) {
+    return CODES == CODES_INT4 ? (p & 1) * 4 + (p >> 1) : p;
+}
+
+template <int CODES, int GS, int G, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+attend_prompt_kernel(const AttArgs A) {
+    using Smem = PromptSmem<D>;
+    constexpr int SB = D / G * (GS == SC_BF16 ? 2 : 1);
+    grid_dependency_begin();
+    extern __shared__ uint8_t prompt_smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(
+        (reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *abort = &sm.abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(&sm.q_full[i], 128);
+            tc::bar_init(&sm.s_full[i], 1);
+            tc::bar_init(&sm.p_full[i], 128);
+            tc::bar_init(&sm.o_full[i], 1);
+            tc::bar_init(&sm.k_full[i], 4);
+            tc::bar_init(&sm.k_empty[i], 1);
+            tc::bar_init(&sm.v_full[i], 4);
+            tc::bar_init(&sm.v_empty[i], 1);
+        }
+        tc::bar_init(&sm.drained, 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) tc::tmem_alloc<512>(&sm.tmem);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = sm.tmem;
+    // columns: S (and P over it) of tile 0, of tile 1, O of tile 0, of tile 1
+    const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 256 + D};
+
+    if (warp < 8) {
+        // ---------------- softmax: thread = row ----------------
+        tc::regs_up<184>();
+        const int t = warp >> 2;
+        const int row_in = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = s_col[t] + lanes, o_addr = o_col[t] + lanes;
+        int done = 0;                               // tiles of this CTA so far (all items)
+        int mine = 0;                               // of them, those of this row tile
+        PromptWalk walk;
+        PromptItem it;
+        bool live = true;
+        while (live && walk.next(A, it, []() {})) {
+            const int row = it.row0 + 128 * t + row_in;
+            const bool valid = row_in < it.rows[t];
+            const int tok = row / A.group;
+            const int64_t qrow = it.s.s0 + tok, qhead = (int64_t)it.head * A.group + row - tok * A.group;
+            float m = -INFINITY, l = 0.0f;
+            const int nt = it.nt[t];
+            if (nt > 0) {
+                // this row of Q, as fp16 scaled so that its largest element is in [2^13, 2^14)
+                uint32_t top = 0;
+                const uint4 *src = reinterpret_cast<const uint4 *>(A.q + qrow * A.q_token + qhead * A.q_head);
+                uint4 raw[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) raw[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+                }
+                const int e = max((int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, -100);
+                const float up = pow2f(13 - e);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        x[2 * k] = __uint_as_float(w[k] << 16) * up;
+                        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+                    }
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = f16x2_rn(x[prompt_order<CODES>(2 * k)], x[prompt_order<CODES>(2 * k + 1)]);
+                    *reinterpret_cast<uint4 *>(sm.q[t] + prompt_off(row_in, i)) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                const float fac = A.scale_log2 * pow2f(e - 13);
+                tc::fence_async();
+                tc::bar_arrive(&sm.q_full[t]);
+                const int lim = valid ? PromptWalk::limit(A, it.s, row) : 0x7fffffff;
+
+                for (int j = 0; j < nt; ++j) {
+                    bool ok = tc::bar_wait(&sm.s_full[t], mine & 1, abort, A.status);
+                    if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+                    tc::fence_after();
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::tmem_load(s_addr + 32 * c, x[c]);
+                    const int slot = (done + j) & 7;
+                    float f[4], ev[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        // (above zero, so that a masked -inf stays -inf)
+                        f[c] = fmaxf(fac * pow2f(sm.ek[slot][c] - kPromptK0), 1e-37f);
+                        ev[c] = (float)sm.ev[slot][c];
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::tmem_load_wait(x[c]);
+                    const int seen = lim - j * kPromptTile;              // columns below it count
+                    if (seen < kPromptTile) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i >= seen) x[c][i] = 0xFF800000u;
+                    }
+                    // row maximum, each 32 positions with their factor and exponent
+                    float top_now = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            a = max3_nan(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                            b = max3_nan(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
+                        }
+                        top_now = max_nan(top_now, fmaf(max_nan(a, b), f[c], ev[c]));
+                    }
+                    // P is at most 2^7 when the maximum is new, 2^15 before it is raised
+                    const float want = top_now - 7.0f;
+                    const bool raise = !(want <= m + 8.0f);
+                    if (j == 0) {
+                        m = want;
+                    } else if (__any_sync(0xffffffffu, raise)) {
+                        const float now = raise ? max_nan(m, want) : m;
+                        const float alpha = (now == m || now == -INFINITY) ? 1.0f : ex2(m - now);
+                        m = now;
+                        l *= alpha;
+                        ok = tc::bar_wait(&sm.o_full[t], (mine - 1) & 1, abort, A.status);
+                        if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+                        tc::fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; ++c) {           // (rare, and short of registers)
+                            uint32_t o[8];
+                            tc::tmem_load8(o_addr + 8 * c, o);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tc::tmem_store8(o_addr + 8 * c, o);
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const f2 ff = bcast(f[c]), off = bcast(ev[c] - mu);
+                        f2 sum = bcast(0.0f);
+                        uint32_t(&p)[32] = x[c & 2];                     // packed over columns already read
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const f2 y = fma2(make_float2(__uint_as_float(x[c][2 * i]),
+                                                          __uint_as_float(x[c][2 * i + 1])), ff, off);
+                            const f2 q = make_float2(ex2(y.x), ex2(y.y));
+                            sum = __fadd2_rn(sum, q);
+                            p[(c & 1) * 16 + i] = f16x2_rn(q.x, q.y);
+                        }
+                        l = fmaf(sum.x + sum.y, pow2f(-(int)ev[c]), l);
+                        if (c & 1) tc::tmem_store(s_addr + 16 * (c - 1), p);
+                    }
+                    tc::tmem_store_wait();
+                    tc::fence_before();
+                    tc::bar_arrive(&sm.p_full[t]);
+                    ++mine;
+                }
+                if (!live) break;
+                const bool ok = tc::bar_wait(&sm.o_full[t], (mine - 1) & 1, abort, A.status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::fence_after();
+            }
+            done += it.steps;
+            // ---- the row of the output
+            if (it.rows[t] > 0) {
+                const float inv = (nt == 0 || m == -INFINITY) ? 0.0f : pow2f(-kPromptK0) / l;
+                uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tc::tmem_load(o_addr + 32 * c, o);
+                        tc::tmem_load_wait(o);
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                y[prompt_order<CODES>(k)] = inv == 0.0f ? 0.0f : __uint_as_float(o[8 * i + k]) * inv;
+                            uint32_t h[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(y[2 * k + 1]), "f"(y[2 * k]));
+                            *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                }
+                tc::fence_before();                 // (these reads before the next item's products)
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------- codes -> fp16 tiles: thread = token ----------------
+        tc::regs_down<104>();
+        const int w = warp - 8, row = w * 32 + lane;
+        int done = 0;
+        PromptWalk walk;
+        PromptItem it;
+        bool live = true;
+        const auto bad = [&]() { if (blockIdx.x == 0 && w == 0 && lane == 0) atomicOr(A.status, STATUS_INDEX); };
+        while (live && walk.next(A, it, bad)) {
+            if (it.steps == 0) continue;
+            const int last = it.row0 + it.rows[0] + it.rows[1] - 1;
+            const int hi = PromptWalk::limit(A, it.s, last);
+            const auto place = [&](int j) -> int64_t {
+                const int pos = j * kPromptTile + row;
+                if (pos >= hi) return -1;
+                const int64_t r = kv_row(A.cache, A.batch, it.seq, pos, it.head);
+                if (r < 0) atomicOr(A.status, STATUS_INDEX);
+                return r;
+            };
+            int64_t at = place(0);
+            uint4 kc[D / 32], vc[D / 32];
+            ScaleWords<SB> ks, vs;
+            prompt_codes<D>(kc, A.cache.k_codes, at);
+            prompt_scales(ks, A.cache.k_scales, at);
+            prompt_scales(vs, A.cache.v_scales, at);
+            for (int j = 0; j < it.steps; ++j) {
+                const int n = done + j, st = n & 1, ph = ((n >> 1) & 1) ^ 1;
+                prompt_codes<D>(vc, A.cache.v_codes, at);
+                // the exponents of both go with the keys: the softmax that
+                // needs them may run before the values are expanded
+                const int ek = max(__reduce_max_sync(0xffffffffu, ks.template top<GS>()), -90);
+                const int ev = max(__reduce_max_sync(0xffffffffu, vs.template top<GS>()), -90);
+                bool ok = n < 2 || tc::bar_wait(&sm.k_empty[st], ph, abort, A.status);
+                if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+                prompt_expand<CODES, GS, G, D, SB>(kc, ks, ek, sm.k[st], row);
+                if (lane == 0) sm.ek[n & 7][w] = ek, sm.ev[n & 7][w] = ev;
+                tc::fence_async();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(&sm.k_full[st]);
+                if (j + 1 < it.steps) {
+                    at = place(j + 1);
+                    prompt_codes<D>(kc, A.cache.k_codes, at);
+                    prompt_scales(ks, A.cache.k_scales, at);
+                }
+                ok = n < 2 || tc::bar_wait(&sm.v_empty[st], ph, abort, A.status);
+                if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+                prompt_expand<CODES, GS, G, D, SB>(vc, vs, ev, sm.v[st], row);
+                tc::fence_async();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(&sm.v_full[st]);
+                if (j + 1 < it.steps) prompt_scales(vs, A.cache.v_scales, at);
+            }
+            done += it.steps;
+        }
+    } else {
+        // ---------------- MMA issue ----------------
+        tc::regs_down<40>();
+        if (warp == 12 && lane == 0) {
+            constexpr uint32_t id_s = tc::idesc_f16(128, 128, false), id_o = tc::idesc_f16(128, D, true);
+            int done = 0, mine[2] = {0, 0}, items[2] = {0, 0};
+            PromptWalk walk;
+            PromptItem it;
+            bool live = true;
+            const auto scores = [&](int t, int st) {
+                const uint32_t a = tc::smem_addr(sm.q[t]), b = tc::smem_addr(sm.k[st]);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
+                    tc::mma_ss(s_col[t], tc::desc_k_major(a + off), tc::desc_k_major(b + off), id_s, kk != 0);
+                }
+                tc::commit(&sm.s_full[t]);
+            };
+            while (live && walk.next(A, it, []() {})) {
+                if (it.steps == 0) continue;
+                for (int j = -1; j < it.steps && live; ++j) {
+                    const int n = done + j;
+                    if (j >= 0) {
+                        live = tc::bar_wait(&sm.v_full[n & 1], (n >> 1) & 1, abort, A.status);
+                        if (!live) break;
+                    }
+                    bool k_ready = false;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (j >= 0 && j < it.nt[t]) {
+                            live = live && tc::bar_wait(&sm.p_full[t], mine[t] & 1, abort, A.status);
+                            if (!live) break;
+                            tc::fence_after();
+                            const uint32_t b = tc::smem_addr(sm.v[n & 1]);
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                tc::mma_ts(o_col[t], s_col[t] + 8 * kk, tc::desc_n_major(b + kk * 2048, 16384),
+                                           id_o, j > 0 || kk > 0);
+                            tc::commit(&sm.o_full[t]);
+                            ++mine[t];
+                        }
+                        if (j + 1 < it.nt[t]) {
+                            if (j < 0) {
+                                live = live && tc::bar_wait(&sm.q_full[t], items[t] & 1, abort, A.status);
+                                ++items[t];
+                            }
+                            if (live && !k_ready) {
+                                const int nk = n + 1;
+                                live = tc::bar_wait(&sm.k_full[nk & 1], (nk >> 1) & 1, abort, A.status);
+                                k_ready = true;
+                            }
+                            if (!live) break;
+                            tc::fence_after();
+                            scores(t, (n + 1) & 1);
+                        }
+                    }
+                    if (!live) break;
+                    if (j >= 0) tc::commit(&sm.v_empty[n & 1]);
+                    if (j + 1 < it.steps) tc::commit(&sm.k_empty[(n + 1) & 1]);
+                }
+                done += it.steps;
+            }
+            // after an abort, products may still be running on this CTA's memory
+            tc::commit(&sm.drained);
+            const uint64_t t0 = tc::now_ns();
+            while (!tc::bar_test(tc::smem_addr(&sm.drained), 0) && tc::now_ns() - t0 <= tc::kWaitLimitNs) {
+            }
+        }
+        __syncwarp();
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc::fence_after();
+        tc::tmem_free<512>(tmem);
+    }
+}
+
+template <int CODES, int GS, int G, int D>
+cudaError_t launch_attend_prompt(AttendLaunch &L) {
+    const AttArgs A = att_args(L, kAttRowsMax);
+    const auto kern = attend_prompt_kernel<CODES, GS, G, D>;
+    constexpr size_t bytes = sizeof(PromptSmem<D>) + 1024;
+    static_assert(bytes <= 232448, "shared memory of the prompt kernel");
+    static std::atomic<bool> done[64];
+    cudaError_t e = smem_opt_in(kern, bytes, done);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = L.tokens * A.group;
+    const int64_t items = ((rows + kPromptRows - 1) / kPromptRows + L.batch.seqs) * L.cache.heads;
+    L.launches = 1;
+    return launch_k(kern, dim3((unsigned)std::min<int64_t>(items, 148)), dim3(kPromptThreads), bytes, L.stream, A);
+}
+
+template <int CODES, int GS, int G, int D>
+cudaError_t launch_attend_d(AttendLaunch &L) {
+    const int64_t rows = L.tokens * (L.q_heads / L.cache.heads);
+    if (rows > 48 * (int64_t)L.batch.seqs) return launch_attend_prompt<CODES, GS, G, D>(L);
+    if (rows <= 8 * (int64_t)L.batch.seqs) return launch_attend_split<CODES, GS, G, D, 1>(L);
+    return launch_attend_split<CODES, GS, G, D, 2>(L);
+}
+
+template <int CODES, int GS>
+cudaError_t launch_attend_fmt(AttendLaunch &L) {
+#define DQ_ATT(GG, DD) \
+    if (L.group == GG && L.cache.head_dim == DD) return launch_attend_d<CODES, GS, GG, DD>(L);
+    DQ_ATT(16, 64) DQ_ATT(32, 64) DQ_ATT(64, 64) DQ_ATT(16, 128) DQ_ATT(32, 128) DQ_ATT(64, 128)
+#undef DQ_ATT
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace dq
