@@ -202,7 +202,6 @@ attend_prompt_kernel(const AttArgs A) {
     tc::fence_after();
     const uint32_t tmem = sm.tmem;
     // columns: S (and P over it) of tile 0, of tile 1, O of tile 0, of tile 1
-    const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 256 + D};
 
     if (warp < 8) {
         // ---------------- softmax: thread = row ----------------
@@ -210,7 +209,7 @@ attend_prompt_kernel(const AttArgs A) {
         const int t = warp >> 2;
         const int row_in = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_addr = s_col[t] + lanes, o_addr = o_col[t] + lanes;
+        const uint32_t s_addr = tmem + 128 * t + lanes, o_addr = tmem + 256 + D * t + lanes;
         int done = 0;                               // tiles of this CTA so far (all items)
         int mine = 0;                               // of them, those of this row tile
         PromptWalk walk;
@@ -218,11 +217,12 @@ attend_prompt_kernel(const AttArgs A) {
         bool live = true;
         while (live && walk.next(A, it, []() {})) {
             const int row = it.row0 + 128 * t + row_in;
-            const bool valid = row_in < it.rows[t];
+            const int rows = t ? it.rows[1] : it.rows[0], nt = t ? it.nt[1] : it.nt[0], steps = it.steps;
+            const bool valid = row_in < rows;
             const int tok = row / A.group;
             const int64_t qrow = it.s.s0 + tok, qhead = (int64_t)it.head * A.group + row - tok * A.group;
+            uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
             float m = -INFINITY, l = 0.0f;
-            const int nt = it.nt[t];
             if (nt > 0) {
                 // this row of Q, as fp16 scaled so that its largest element is in [2^13, 2^14)
                 uint32_t top = 0;
@@ -344,11 +344,10 @@ attend_prompt_kernel(const AttArgs A) {
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::fence_after();
             }
-            done += it.steps;
+            done += steps;
             // ---- the row of the output
-            if (it.rows[t] > 0) {
+            if (rows > 0) {
                 const float inv = (nt == 0 || m == -INFINITY) ? 0.0f : pow2f(-kPromptK0) / l;
-                uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -394,9 +393,11 @@ attend_prompt_kernel(const AttArgs A) {
                 if (r < 0) atomicOr(A.status, STATUS_INDEX);
                 return r;
             };
-            int64_t at = place(0);
+            // loads run ahead: a tile's rows are looked up two tiles before
+            // it is expanded, its scales and key codes loaded one before
+            int64_t at = place(0), at_next = place(1);
             uint4 kc[D / 32], vc[D / 32];
-            ScaleWords<SB> ks, vs;
+            ScaleWords<SB> ks, vs, vs_next;
             prompt_codes<D>(kc, A.cache.k_codes, at);
             prompt_scales(ks, A.cache.k_scales, at);
             prompt_scales(vs, A.cache.v_scales, at);
@@ -414,85 +415,104 @@ attend_prompt_kernel(const AttArgs A) {
                 tc::fence_async();
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(&sm.k_full[st]);
-                if (j + 1 < it.steps) {
-                    at = place(j + 1);
-                    prompt_codes<D>(kc, A.cache.k_codes, at);
-                    prompt_scales(ks, A.cache.k_scales, at);
-                }
+                at = at_next;
+                prompt_codes<D>(kc, A.cache.k_codes, at);
+                prompt_scales(ks, A.cache.k_scales, at);
+                prompt_scales(vs_next, A.cache.v_scales, at);
+                at_next = place(j + 2);
                 ok = n < 2 || tc::bar_wait(&sm.v_empty[st], ph, abort, A.status);
                 if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
                 prompt_expand<CODES, GS, G, D, SB>(vc, vs, ev, sm.v[st], row);
                 tc::fence_async();
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(&sm.v_full[st]);
-                if (j + 1 < it.steps) prompt_scales(vs, A.cache.v_scales, at);
+                vs = vs_next;
             }
             done += it.steps;
         }
     } else {
         // ---------------- MMA issue ----------------
         tc::regs_down<40>();
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {
             constexpr uint32_t id_s = tc::idesc_f16(128, 128, false), id_o = tc::idesc_f16(128, D, true);
-            int done = 0, mine[2] = {0, 0}, items[2] = {0, 0};
+            int done = 0;
+            uint32_t phases = 0;                     // bit t: of p_full[t]; bit 2 + t: of q_full[t]
             PromptWalk walk;
             PromptItem it;
             bool live = true;
+            const auto wait = [&](uint64_t *bar, int phase) {
+                live = live && __all_sync(0xffffffffu, tc::bar_wait(bar, phase & 1, abort, A.status));
+                return live;
+            };
+            // (loops, so that no table of descriptors is kept in registers)
+            const uint64_t q_desc = tc::desc_k_major(tc::smem_addr(sm.q[0])), k_desc = tc::desc_k_major(tc::smem_addr(sm.k[0]));
+            const uint64_t v_desc = tc::desc_n_major(tc::smem_addr(sm.v[0]), 16384);
+            constexpr uint32_t kStep = 128 * D * 2 / 16;             // one tile, in descriptor units
             const auto scores = [&](int t, int st) {
-                const uint32_t a = tc::smem_addr(sm.q[t]), b = tc::smem_addr(sm.k[st]);
+                if (tc::elect()) {
+                    uint64_t a = q_desc + t * kStep, b = k_desc + st * kStep;
+#pragma unroll 1
+                    for (int h = 0; h < D / 64; ++h, a += 1024, b += 1024) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
-                    tc::mma_ss(s_col[t], tc::desc_k_major(a + off), tc::desc_k_major(b + off), id_s, kk != 0);
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_ss(tmem + 128 * t, a + 2 * kk, b + 2 * kk, id_s, h + kk != 0);
+                    }
+                    tc::commit(&sm.s_full[t]);
                 }
-                tc::commit(&sm.s_full[t]);
+                __syncwarp();
+            };
+            const auto sums = [&](int t, int st, bool more) {
+                if (tc::elect()) {
+                    uint64_t b = v_desc + st * kStep;
+                    uint32_t p = tmem + 128 * t;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h, b += 4 * 128, p += 32) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_ts(tmem + 256 + D * t, p + 8 * kk, b + 128 * kk, id_o, more || h + kk != 0);
+                    }
+                    tc::commit(&sm.o_full[t]);
+                }
+                __syncwarp();
             };
             while (live && walk.next(A, it, []() {})) {
                 if (it.steps == 0) continue;
                 for (int j = -1; j < it.steps && live; ++j) {
-                    const int n = done + j;
-                    if (j >= 0) {
-                        live = tc::bar_wait(&sm.v_full[n & 1], (n >> 1) & 1, abort, A.status);
-                        if (!live) break;
-                    }
+                    const int n = done + j;                          // of the values; the keys are one ahead
+                    if (j >= 0 && !wait(&sm.v_full[n & 1], n >> 1)) break;
                     bool k_ready = false;
-#pragma unroll
+#pragma unroll 1
                     for (int t = 0; t < 2; ++t) {
-                        if (j >= 0 && j < it.nt[t]) {
-                            live = live && tc::bar_wait(&sm.p_full[t], mine[t] & 1, abort, A.status);
-                            if (!live) break;
+                        const int nt = t ? it.nt[1] : it.nt[0];
+                        if (live && j >= 0 && j < nt && wait(&sm.p_full[t], phases >> t)) {
+                            phases ^= 1u << t;
                             tc::fence_after();
-                            const uint32_t b = tc::smem_addr(sm.v[n & 1]);
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                tc::mma_ts(o_col[t], s_col[t] + 8 * kk, tc::desc_n_major(b + kk * 2048, 16384),
-                                           id_o, j > 0 || kk > 0);
-                            tc::commit(&sm.o_full[t]);
-                            ++mine[t];
+                            sums(t, n & 1, j > 0);
                         }
-                        if (j + 1 < it.nt[t]) {
+                        if (live && j + 1 < nt) {
                             if (j < 0) {
-                                live = live && tc::bar_wait(&sm.q_full[t], items[t] & 1, abort, A.status);
-                                ++items[t];
+                                wait(&sm.q_full[t], phases >> (2 + t));
+                                phases ^= 4u << t;
                             }
-                            if (live && !k_ready) {
-                                const int nk = n + 1;
-                                live = tc::bar_wait(&sm.k_full[nk & 1], (nk >> 1) & 1, abort, A.status);
-                                k_ready = true;
+                            if (!k_ready) wait(&sm.k_full[(n + 1) & 1], (n + 1) >> 1);
+                            k_ready = true;
+                            if (live) {
+                                tc::fence_after();
+                                scores(t, (n + 1) & 1);
                             }
-                            if (!live) break;
-                            tc::fence_after();
-                            scores(t, (n + 1) & 1);
                         }
                     }
-                    if (!live) break;
-                    if (j >= 0) tc::commit(&sm.v_empty[n & 1]);
-                    if (j + 1 < it.steps) tc::commit(&sm.k_empty[(n + 1) & 1]);
+                    if (live && tc::elect()) {
+                        if (j >= 0) tc::commit(&sm.v_empty[n & 1]);
+                        if (j + 1 < it.steps) tc::commit(&sm.k_empty[(n + 1) & 1]);
+                    }
+                    __syncwarp();
                 }
                 done += it.steps;
             }
             // after an abort, products may still be running on this CTA's memory
-            tc::commit(&sm.drained);
+            if (tc::elect()) tc::commit(&sm.drained);
+            __syncwarp();
             const uint64_t t0 = tc::now_ns();
             while (!tc::bar_test(tc::smem_addr(&sm.drained), 0) && tc::now_ns() - t0 <= tc::kWaitLimitNs) {
             }

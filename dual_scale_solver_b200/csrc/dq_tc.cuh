@@ -70,6 +70,15 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
                  :: "r"(smem_addr(bar)) : "memory");
 }
 
+// One lane of a converged warp (the same one each time).  MMAs and commits are
+// issued under it by a warp that computes their operands together, so that
+// they stay in uniform registers.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+
 // ---- operands.  Tiles of fp16 in shared memory are blocks of 64 contiguous
 // elements (128 bytes, 128-byte swizzle) by rows, 8-row groups 1024 bytes
 // apart.
