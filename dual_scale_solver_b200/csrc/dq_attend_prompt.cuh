@@ -41,21 +41,8 @@ namespace dq {
 
 constexpr int kPromptRows = 256;                 // query rows of a CTA
 constexpr int kPromptTile = 128;                 // positions per step
-constexpr int kPromptThreads = 512;
+constexpr int kPromptThreads = 416;
 constexpr int kPromptK0 = 12;                    // fp16 code x scale: at most 7 * 2^13
-
-template <int D>
-struct __align__(1024) PromptSmem {
-    uint8_t q[2][128 * D * 2];
-    uint8_t k[2][128 * D * 2];
-    uint8_t v[2][128 * D * 2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];     // by row tile
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // by stage
-    uint64_t drained;
-    int ek[8][4], ev[8][4];                      // exponents by tile (mod 8) and 32 tokens
-    uint32_t tmem;
-    int abort;
-};
 
 // Byte of 16-byte chunk c (8 elements) of a row in a tile of 128 rows.
 __device__ __forceinline__ uint32_t prompt_off(int row, int c) {
@@ -69,43 +56,51 @@ struct PromptItem {
     int steps;
 };
 
-// The CTA's items, one per call: a sequence's row tiles go from the last
+// The CTA's items, one per step: a sequence's row tiles go from the last
 // (longest, when causal) to the first, all heads of each; rounds of the grid
 // run forwards and backwards in turn, so that long and short ones pair up.
 struct PromptWalk {
-    int seq = 0, round = 0;
-    long long first = 0;
-    template <class F>
-    __device__ __forceinline__ bool next(const AttArgs &A, PromptItem &it, F bad) {
+    int seq, round;
+    long long first;
+    PromptItem it;
+    // The next item, for the whole warp whose walk this is (in shared memory,
+    // worked out by one lane: registers are short elsewhere).
+    __device__ __forceinline__ bool next(const AttArgs &A, bool report) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) step(A, report);
+        __syncwarp();
+        return it.seq >= 0;
+    }
+    __device__ __forceinline__ void step(const AttArgs &A, bool report) {
         const long long n = gridDim.x;
         const long long idx = round * n + ((round & 1) ? n - 1 - blockIdx.x : blockIdx.x);
         ++round;
         for (; seq < A.batch.seqs; ++seq) {
-            it.s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
-            if (!it.s.ok) bad();
-            const int all = it.s.n * A.group;
+            const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
+            if (!s.ok && report) atomicOr(A.status, STATUS_INDEX);
+            const int all = s.n * A.group;
             const int tiles = (all + kPromptRows - 1) / kPromptRows;
             const long long cnt = (long long)tiles * A.cache.heads;
             if (idx < first + cnt) {
                 const long long local = idx - first;
                 const int up = (int)(local / A.cache.heads);
+                it.s = s;
                 it.seq = seq;
                 it.head = (int)(local - (long long)up * A.cache.heads);
                 it.row0 = (tiles - 1 - up) * kPromptRows;
                 it.steps = 0;
-#pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int r0 = it.row0 + 128 * t;
                     it.rows[t] = min(max(all - r0, 0), 128);
                     it.nt[t] = it.rows[t] == 0 ? 0
-                                               : (limit(A, it.s, r0 + it.rows[t] - 1) + kPromptTile - 1) / kPromptTile;
+                                               : (limit(A, s, r0 + it.rows[t] - 1) + kPromptTile - 1) / kPromptTile;
                     it.steps = max(it.steps, it.nt[t]);
                 }
-                return true;
+                return;
             }
             first += cnt;
         }
-        return false;
+        it.seq = -1;
     }
     // positions below it are seen by the row
     __device__ __forceinline__ static int limit(const AttArgs &A, const KvSeq &s, int row) {
@@ -113,12 +108,35 @@ struct PromptWalk {
     }
 };
 
-// One token's codes of one head, and its scales (zeros for row < 0).
+template <int D>
+struct __align__(1024) PromptSmem {
+    uint8_t q[2][128 * D * 2];
+    uint8_t k[2][128 * D * 2];
+    uint8_t v[2][128 * D * 2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];     // by row tile
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // by stage
+    uint64_t drained;
+    // of a position tile (mod 8) and 32 of its tokens: 2^(E - k0) of the
+    // keys, E and 2^-E of the values
+    float kf[8][4], ve[8][4], vi[8][4];
+    PromptWalk walk[13];                         // of each warp
+    uint32_t tmem;
+    int abort;
+};
+
+// One token's codes of one head (passing L1 by), and its scales (zeros for
+// row < 0).
+__device__ __forceinline__ uint4 prompt_load(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 template <int D>
 __device__ __forceinline__ void prompt_codes(uint4 (&c)[D / 32], const uint8_t *codes, int64_t row) {
     const uint4 *p = reinterpret_cast<const uint4 *>(codes + row * (D / 2));
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) c[i] = row >= 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < D / 32; ++i) c[i] = row >= 0 ? prompt_load(p + i) : make_uint4(0, 0, 0, 0);
 }
 template <int SB>
 __device__ __forceinline__ void prompt_scales(ScaleWords<SB> &s, const void *scales, int64_t row) {
@@ -196,6 +214,8 @@ attend_prompt_kernel(const AttArgs A) {
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (lane == 0) sm.walk[warp].seq = 0, sm.walk[warp].round = 0, sm.walk[warp].first = 0;
+    const PromptItem &it = sm.walk[warp].it;
     if (warp == 12) tc::tmem_alloc<512>(&sm.tmem);
     tc::fence_before();
     __syncthreads();
@@ -205,42 +225,35 @@ attend_prompt_kernel(const AttArgs A) {
 
     if (warp < 8) {
         // ---------------- softmax: thread = row ----------------
-        tc::regs_up<184>();
         const int t = warp >> 2;
-        const int row_in = threadIdx.x & 127;
+        const int row_in = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + 128 * t + lanes, o_addr = tmem + 256 + D * t + lanes;
         int done = 0;                               // tiles of this CTA so far (all items)
         int mine = 0;                               // of them, those of this row tile
-        PromptWalk walk;
-        PromptItem it;
         bool live = true;
-        while (live && walk.next(A, it, []() {})) {
+        while (live && sm.walk[warp].next(A, false)) {
             const int row = it.row0 + 128 * t + row_in;
-            const int rows = t ? it.rows[1] : it.rows[0], nt = t ? it.nt[1] : it.nt[0], steps = it.steps;
-            const bool valid = row_in < rows;
+            const int nt = it.nt[t];
+            const bool valid = row_in < it.rows[t];
             const int tok = row / A.group;
             const int64_t qrow = it.s.s0 + tok, qhead = (int64_t)it.head * A.group + row - tok * A.group;
-            uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
             float m = -INFINITY, l = 0.0f;
             if (nt > 0) {
                 // this row of Q, as fp16 scaled so that its largest element is in [2^13, 2^14)
                 uint32_t top = 0;
                 const uint4 *src = reinterpret_cast<const uint4 *>(A.q + qrow * A.q_token + qhead * A.q_head);
-                uint4 raw[D / 8];
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) raw[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+                    const uint4 v = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    top = __vmaxu2(__vmaxu2(top, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
                 }
                 const int e = max((int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, -100);
                 const float up = pow2f(13 - e);
-#pragma unroll
+#pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    const uint4 v = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     float x[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -256,83 +269,92 @@ attend_prompt_kernel(const AttArgs A) {
                 const float fac = A.scale_log2 * pow2f(e - 13);
                 tc::fence_async();
                 tc::bar_arrive(&sm.q_full[t]);
-                const int lim = valid ? PromptWalk::limit(A, it.s, row) : 0x7fffffff;
+                int seen = valid ? PromptWalk::limit(A, it.s, row) : 0x7fffffff;   // columns below it count
 
-                for (int j = 0; j < nt; ++j) {
+                for (int j = 0; j < nt; ++j, seen -= kPromptTile) {
                     bool ok = tc::bar_wait(&sm.s_full[t], mine & 1, abort, A.status);
                     if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
                     tc::fence_after();
-                    uint32_t x[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::tmem_load(s_addr + 32 * c, x[c]);
                     const int slot = (done + j) & 7;
-                    float f[4], ev[4];
+                    // 64 columns at a time, and read twice (for the maximum and
+                    // for P): a read takes some 30 clocks, a spilled register
+                    // ten times that
+                    uint32_t x[2][32];
+                    const auto columns = [&](int h) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        // (above zero, so that a masked -inf stays -inf)
-                        f[c] = fmaxf(fac * pow2f(sm.ek[slot][c] - kPromptK0), 1e-37f);
-                        ev[c] = (float)sm.ev[slot][c];
-                    }
+                        for (int c = 0; c < 2; ++c) tc::tmem_load(s_addr + 64 * h + 32 * c, x[c]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::tmem_load_wait(x[c]);
-                    const int seen = lim - j * kPromptTile;              // columns below it count
-                    if (seen < kPromptTile) {
+                        for (int c = 0; c < 2; ++c) tc::tmem_load_wait(x[c]);
+                        if (seen < 64 * (h + 1)) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (32 * c + i >= seen) x[c][i] = 0xFF800000u;
-                    }
-                    // row maximum, each 32 positions with their factor and exponent
-                    float top_now = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            a = max3_nan(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-                            b = max3_nan(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
+                                for (int i = 0; i < 32; ++i)
+                                    if (64 * h + 32 * c + i >= seen) x[c][i] = 0xFF800000u;
                         }
-                        top_now = max_nan(top_now, fmaf(max_nan(a, b), f[c], ev[c]));
+                    };
+                    // (above zero, so that a masked -inf stays -inf)
+                    const auto factor = [&](int c) { return fmaxf(fac * sm.kf[slot][c], 1e-37f); };
+                    // row maximum, each 32 positions with their factor and exponent
+                    float want = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        columns(h);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                a = max3_nan(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                                b = max3_nan(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
+                            }
+                            want = max_nan(want, fmaf(max_nan(a, b), factor(2 * h + c), sm.ve[slot][2 * h + c]));
+                        }
                     }
                     // P is at most 2^7 when the maximum is new, 2^15 before it is raised
-                    const float want = top_now - 7.0f;
-                    const bool raise = !(want <= m + 8.0f);
-                    if (j == 0) {
-                        m = want;
-                    } else if (__any_sync(0xffffffffu, raise)) {
-                        const float now = raise ? max_nan(m, want) : m;
-                        const float alpha = (now == m || now == -INFINITY) ? 1.0f : ex2(m - now);
+                    want -= 7.0f;
+                    if (__any_sync(0xffffffffu, want > m + 8.0f)) {
+                        const float now = want > m + 8.0f ? want : m;
+                        const float alpha = now == m ? 1.0f : ex2(m - now);
                         m = now;
                         l *= alpha;
-                        ok = tc::bar_wait(&sm.o_full[t], (mine - 1) & 1, abort, A.status);
-                        if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
-                        tc::fence_after();
+                        if (j > 0) {
+                            ok = tc::bar_wait(&sm.o_full[t], (mine - 1) & 1, abort, A.status);
+                            if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+                            tc::fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 8; ++c) {           // (rare, and short of registers)
-                            uint32_t o[8];
-                            tc::tmem_load8(o_addr + 8 * c, o);
+                            for (int c = 0; c < D / 8; ++c) {
+                                uint32_t o[8];
+                                tc::tmem_load8(o_addr + 8 * c, o);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tc::tmem_store8(o_addr + 8 * c, o);
+                                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                tc::tmem_store8(o_addr + 8 * c, o);
+                            }
                         }
                     }
                     const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const f2 ff = bcast(f[c]), off = bcast(ev[c] - mu);
-                        f2 sum = bcast(0.0f);
-                        uint32_t(&p)[32] = x[c & 2];                     // packed over columns already read
+                    for (int h = 0; h < 2; ++h) {
+                        columns(h);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const f2 y = fma2(make_float2(__uint_as_float(x[c][2 * i]),
-                                                          __uint_as_float(x[c][2 * i + 1])), ff, off);
-                            const f2 q = make_float2(ex2(y.x), ex2(y.y));
-                            sum = __fadd2_rn(sum, q);
-                            p[(c & 1) * 16 + i] = f16x2_rn(q.x, q.y);
+                        for (int c = 0; c < 2; ++c) {
+                            const float f = factor(2 * h + c), off = sm.ve[slot][2 * h + c] - mu;
+                            float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                uint32_t p[8];                          // over columns already read
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float p0 = ex2(fmaf(__uint_as_float(x[c][16 * g + 2 * i]), f, off));
+                                    const float p1 = ex2(fmaf(__uint_as_float(x[c][16 * g + 2 * i + 1]), f, off));
+                                    sum0 += p0;
+                                    sum1 += p1;
+                                    p[i] = f16x2_rn(p0, p1);
+                                }
+                                tc::tmem_store8(s_addr + 32 * h + 16 * c + 8 * g, p);
+                            }
+                            l = fmaf(sum0 + sum1, sm.vi[slot][2 * h + c], l);
                         }
-                        l = fmaf(sum.x + sum.y, pow2f(-(int)ev[c]), l);
-                        if (c & 1) tc::tmem_store(s_addr + 16 * (c - 1), p);
                     }
                     tc::tmem_store_wait();
                     tc::fence_before();
@@ -344,30 +366,25 @@ attend_prompt_kernel(const AttArgs A) {
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::fence_after();
             }
-            done += steps;
+            done += it.steps;
             // ---- the row of the output
-            if (rows > 0) {
+            if (it.rows[t] > 0) {
                 const float inv = (nt == 0 || m == -INFINITY) ? 0.0f : pow2f(-kPromptK0) / l;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    if (nt > 0) {
-                        tc::tmem_load(o_addr + 32 * c, o);
-                        tc::tmem_load_wait(o);
-                    }
+                uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
+#pragma unroll 2
+                for (int c = 0; c < D / 8; ++c) {
+                    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (nt > 0) tc::tmem_load8(o_addr + 8 * c, o);
                     if (valid) {
+                        float y[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float y[8];
+                        for (int k = 0; k < 8; ++k)
+                            y[prompt_order<CODES>(k)] = inv == 0.0f ? 0.0f : __uint_as_float(o[k]) * inv;
+                        uint32_t h[4];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                y[prompt_order<CODES>(k)] = inv == 0.0f ? 0.0f : __uint_as_float(o[8 * i + k]) * inv;
-                            uint32_t h[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(y[2 * k + 1]), "f"(y[2 * k]));
-                            *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(y[2 * k + 1]), "f"(y[2 * k]));
+                        *reinterpret_cast<uint4 *>(dst + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
                 tc::fence_before();                 // (these reads before the next item's products)
@@ -375,14 +392,10 @@ attend_prompt_kernel(const AttArgs A) {
         }
     } else if (warp < 12) {
         // ---------------- codes -> fp16 tiles: thread = token ----------------
-        tc::regs_down<104>();
         const int w = warp - 8, row = w * 32 + lane;
         int done = 0;
-        PromptWalk walk;
-        PromptItem it;
         bool live = true;
-        const auto bad = [&]() { if (blockIdx.x == 0 && w == 0 && lane == 0) atomicOr(A.status, STATUS_INDEX); };
-        while (live && walk.next(A, it, bad)) {
+        while (live && sm.walk[warp].next(A, blockIdx.x == 0 && w == 0)) {
             if (it.steps == 0) continue;
             const int last = it.row0 + it.rows[0] + it.rows[1] - 1;
             const int hi = PromptWalk::limit(A, it.s, last);
@@ -411,7 +424,11 @@ attend_prompt_kernel(const AttArgs A) {
                 bool ok = n < 2 || tc::bar_wait(&sm.k_empty[st], ph, abort, A.status);
                 if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
                 prompt_expand<CODES, GS, G, D, SB>(kc, ks, ek, sm.k[st], row);
-                if (lane == 0) sm.ek[n & 7][w] = ek, sm.ev[n & 7][w] = ev;
+                if (lane == 0) {
+                    sm.kf[n & 7][w] = pow2f(ek - kPromptK0);
+                    sm.ve[n & 7][w] = (float)ev;
+                    sm.vi[n & 7][w] = pow2f(-ev);
+                }
                 tc::fence_async();
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(&sm.k_full[st]);
@@ -432,38 +449,22 @@ attend_prompt_kernel(const AttArgs A) {
         }
     } else {
         // ---------------- MMA issue ----------------
-        tc::regs_down<40>();
-        if (warp == 12) {
-            constexpr uint32_t id_s = tc::idesc_f16(128, 128, false), id_o = tc::idesc_f16(128, D, true);
-            int done = 0;
-            uint32_t phases = 0;                     // bit t: of p_full[t]; bit 2 + t: of q_full[t]
-            PromptWalk walk;
-            PromptItem it;
-            bool live = true;
-            const auto wait = [&](uint64_t *bar, int phase) {
-                live = live && __all_sync(0xffffffffu, tc::bar_wait(bar, phase & 1, abort, A.status));
-                return live;
-            };
-            // (loops, so that no table of descriptors is kept in registers)
-            const uint64_t q_desc = tc::desc_k_major(tc::smem_addr(sm.q[0])), k_desc = tc::desc_k_major(tc::smem_addr(sm.k[0]));
-            const uint64_t v_desc = tc::desc_n_major(tc::smem_addr(sm.v[0]), 16384);
-            constexpr uint32_t kStep = 128 * D * 2 / 16;             // one tile, in descriptor units
-            const auto scores = [&](int t, int st) {
-                if (tc::elect()) {
-                    uint64_t a = q_desc + t * kStep, b = k_desc + st * kStep;
-#pragma unroll 1
-                    for (int h = 0; h < D / 64; ++h, a += 1024, b += 1024) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_ss(tmem + 128 * t, a + 2 * kk, b + 2 * kk, id_s, h + kk != 0);
-                    }
-                    tc::commit(&sm.s_full[t]);
-                }
-                __syncwarp();
-            };
-            const auto sums = [&](int t, int st, bool more) {
-                if (tc::elect()) {
-                    uint64_t b = v_desc + st * kStep;
+        constexpr uint32_t id_s = tc::idesc_f16(128, 128, false), id_o = tc::idesc_f16(128, D, true);
+        int done = 0;
+        uint32_t phases = 0;                         // bit t: of p_full[t]; bit 2 + t: of q_full[t]
+        bool live = true;
+        const auto wait = [&](uint64_t *bar, int phase) {
+            live = live && __all_sync(0xffffffffu, tc::bar_wait(bar, phase & 1, abort, A.status));
+        };
+        constexpr uint32_t kStep = 128 * D * 2 / 16;                 // one tile, in descriptor units
+        const uint64_t q_desc = tc::desc_k_major(tc::smem_addr(sm.q[0])), k_desc = tc::desc_k_major(tc::smem_addr(sm.k[0]));
+        const uint64_t v_desc = tc::desc_n_major(tc::smem_addr(sm.v[0]), 16384);
+        // O += P V for the values of stage sv, S = Q K^T for the keys of stage
+        // sk (loops, so that no table of descriptors is kept in registers)
+        const auto issue = [&](int t, bool sums, int sv, bool more, bool scores, int sk) {
+            if (tc::elect()) {
+                if (sums) {
+                    uint64_t b = v_desc + sv * kStep;
                     uint32_t p = tmem + 128 * t;
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h, b += 4 * 128, p += 32) {
@@ -473,49 +474,55 @@ attend_prompt_kernel(const AttArgs A) {
                     }
                     tc::commit(&sm.o_full[t]);
                 }
-                __syncwarp();
-            };
-            while (live && walk.next(A, it, []() {})) {
-                if (it.steps == 0) continue;
-                for (int j = -1; j < it.steps && live; ++j) {
-                    const int n = done + j;                          // of the values; the keys are one ahead
-                    if (j >= 0 && !wait(&sm.v_full[n & 1], n >> 1)) break;
-                    bool k_ready = false;
+                if (scores) {
+                    uint64_t a = q_desc + t * kStep, b = k_desc + sk * kStep;
 #pragma unroll 1
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = t ? it.nt[1] : it.nt[0];
-                        if (live && j >= 0 && j < nt && wait(&sm.p_full[t], phases >> t)) {
-                            phases ^= 1u << t;
-                            tc::fence_after();
-                            sums(t, n & 1, j > 0);
-                        }
-                        if (live && j + 1 < nt) {
-                            if (j < 0) {
-                                wait(&sm.q_full[t], phases >> (2 + t));
-                                phases ^= 4u << t;
-                            }
-                            if (!k_ready) wait(&sm.k_full[(n + 1) & 1], (n + 1) >> 1);
-                            k_ready = true;
-                            if (live) {
-                                tc::fence_after();
-                                scores(t, (n + 1) & 1);
-                            }
-                        }
+                    for (int h = 0; h < D / 64; ++h, a += 1024, b += 1024) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_ss(tmem + 128 * t, a + 2 * kk, b + 2 * kk, id_s, h + kk != 0);
                     }
-                    if (live && tc::elect()) {
-                        if (j >= 0) tc::commit(&sm.v_empty[n & 1]);
-                        if (j + 1 < it.steps) tc::commit(&sm.k_empty[(n + 1) & 1]);
-                    }
-                    __syncwarp();
+                    tc::commit(&sm.s_full[t]);
                 }
-                done += it.steps;
             }
-            // after an abort, products may still be running on this CTA's memory
-            if (tc::elect()) tc::commit(&sm.drained);
             __syncwarp();
-            const uint64_t t0 = tc::now_ns();
-            while (!tc::bar_test(tc::smem_addr(&sm.drained), 0) && tc::now_ns() - t0 <= tc::kWaitLimitNs) {
+        };
+        while (live && sm.walk[warp].next(A, false)) {
+            const int steps = it.steps, nt0 = it.nt[0], nt1 = it.nt[1];
+            for (int j = -1; j < steps && live; ++j) {
+                const int n = done + j;                              // of the values; the keys are one ahead
+                // both tiles are ready long before the rows are
+                if (j >= 0) wait(&sm.v_full[n & 1], n >> 1);
+                if (j + 1 < steps) wait(&sm.k_full[(n + 1) & 1], (n + 1) >> 1);
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    const int nt = t ? nt1 : nt0;
+                    const bool sums = j >= 0 && j < nt, scores = j + 1 < nt;
+                    if (sums) {
+                        wait(&sm.p_full[t], phases >> t);
+                        phases ^= 1u << t;
+                    } else if (scores) {
+                        wait(&sm.q_full[t], phases >> (2 + t));
+                        phases ^= 4u << t;
+                    }
+                    if (live && (sums || scores)) {
+                        tc::fence_after();
+                        issue(t, sums, n & 1, j > 0, scores, (n + 1) & 1);
+                    }
+                }
+                if (live && tc::elect()) {
+                    if (j >= 0) tc::commit(&sm.v_empty[n & 1]);
+                    if (j + 1 < steps) tc::commit(&sm.k_empty[(n + 1) & 1]);
+                }
+                __syncwarp();
             }
+            done += steps;
+        }
+        // after an abort, products may still be running on this CTA's memory
+        if (tc::elect()) tc::commit(&sm.drained);
+        __syncwarp();
+        const uint64_t t0 = tc::now_ns();
+        while (!tc::bar_test(tc::smem_addr(&sm.drained), 0) && tc::now_ns() - t0 <= tc::kWaitLimitNs) {
         }
         __syncwarp();
     }

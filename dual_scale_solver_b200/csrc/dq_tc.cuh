@@ -53,6 +53,19 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile 
     return false;
 }
 
+// ---- named barriers of some warps (every thread of them arrives)
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync.aligned %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+// whether the predicate holds in any of the threads
+__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %3, 0;\n\t"
+                 "barrier.cta.red.or.pred.aligned q, %1, %2, p; selp.u32 %0, 1, 0, q; }"
+                 : "=r"(r) : "r"(id), "r"(threads), "r"((uint32_t)v) : "memory");
+    return r != 0;
+}
+
 // ---- ordering
 __device__ __forceinline__ void fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
