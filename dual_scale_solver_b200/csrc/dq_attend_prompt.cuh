@@ -30,7 +30,7 @@
 //                    bring in the row of Q and write the row of the output
 //   warps 8-11       codes -> fp16 tiles: a thread per token, 64 bytes of
 //                    codes in registers while the previous tile is expanded
-//   warp 12          issues the MMAs
+//   warps 12, 13     issue the MMAs of row tile 0, 1
 // Every wait is bounded (dq_tc.cuh).
 #pragma once
 
@@ -40,8 +40,9 @@
 namespace dq {
 
 constexpr int kPromptRows = 256;                 // query rows of a CTA
-constexpr int kPromptTile = 128;                 // positions per step
-constexpr int kPromptThreads = 416;
+constexpr int kPromptTile = 128;                 // positions of a tile of keys or values
+constexpr int kPromptStep = 64;                  // positions of a step of the softmax
+constexpr int kPromptThreads = 448;
 constexpr int kPromptK0 = 12;                    // fp16 code x scale: at most 7 * 2^13
 
 // Byte of 16-byte chunk c (8 elements) of a row in a tile of 128 rows.
@@ -52,8 +53,8 @@ __device__ __forceinline__ uint32_t prompt_off(int row, int c) {
 struct PromptItem {
     KvSeq s;
     int seq, head, row0;
-    int rows[2], nt[2];                          // valid rows and position tiles of each row tile
-    int steps;
+    int rows[2], nt[2];                          // valid rows and steps of positions of each row tile
+    int steps;                                   // tiles of positions
 };
 
 // The CTA's items, one per step: a sequence's row tiles go from the last
@@ -93,8 +94,8 @@ struct PromptWalk {
                     const int r0 = it.row0 + 128 * t;
                     it.rows[t] = min(max(all - r0, 0), 128);
                     it.nt[t] = it.rows[t] == 0 ? 0
-                                               : (limit(A, s, r0 + it.rows[t] - 1) + kPromptTile - 1) / kPromptTile;
-                    it.steps = max(it.steps, it.nt[t]);
+                                               : (limit(A, s, r0 + it.rows[t] - 1) + kPromptStep - 1) / kPromptStep;
+                    it.steps = max(it.steps, (it.nt[t] + 1) / 2);
                 }
                 return;
             }
@@ -113,13 +114,14 @@ struct __align__(1024) PromptSmem {
     uint8_t q[2][128 * D * 2];
     uint8_t k[2][128 * D * 2];
     uint8_t v[2][128 * D * 2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];     // by row tile
+    uint64_t q_full[2];                                      // by row tile
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2];       // by row tile and half of its score columns
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // by stage
-    uint64_t drained;
+    uint64_t drained[2];
     // of a position tile (mod 8) and 32 of its tokens: 2^(E - k0) of the
     // keys, E and 2^-E of the values
     float kf[8][4], ve[8][4], vi[8][4];
-    PromptWalk walk[13];                         // of each warp
+    PromptWalk walk[14];                         // of each warp
     uint32_t tmem;
     int abort;
 };
@@ -202,15 +204,17 @@ attend_prompt_kernel(const AttArgs A) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(&sm.q_full[i], 128);
-            tc::bar_init(&sm.s_full[i], 1);
-            tc::bar_init(&sm.p_full[i], 128);
-            tc::bar_init(&sm.o_full[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                tc::bar_init(&sm.s_full[i][b], 1);
+                tc::bar_init(&sm.p_full[i][b], 128);
+                tc::bar_init(&sm.o_full[i][b], 1);
+            }
+            tc::bar_init(&sm.drained[i], 1);
             tc::bar_init(&sm.k_full[i], 4);
-            tc::bar_init(&sm.k_empty[i], 1);
+            tc::bar_init(&sm.k_empty[i], 2);
             tc::bar_init(&sm.v_full[i], 4);
-            tc::bar_init(&sm.v_empty[i], 1);
+            tc::bar_init(&sm.v_empty[i], 2);
         }
-        tc::bar_init(&sm.drained, 1);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -229,9 +233,15 @@ attend_prompt_kernel(const AttArgs A) {
         const int row_in = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + 128 * t + lanes, o_addr = tmem + 256 + D * t + lanes;
-        int done = 0;                               // tiles of this CTA so far (all items)
-        int mine = 0;                               // of them, those of this row tile
+        int done = 0;                               // position tiles of this CTA so far (all items)
+        int mine = 0;                               // steps of this row tile so far
         bool live = true;
+        // the product of the step before this one is in O (of the two steps'
+        // barriers in turn: the one before that is, since its scores' columns
+        // have been used again)
+        const auto summed = [&]() {
+            return tc::bar_wait(&sm.o_full[t][(mine - 1) & 1], ((mine - 1) >> 1) & 1, abort, A.status);
+        };
         while (live && sm.walk[warp].next(A, false)) {
             const int row = it.row0 + 128 * t + row_in;
             const int nt = it.nt[t];
@@ -271,45 +281,43 @@ attend_prompt_kernel(const AttArgs A) {
                 tc::bar_arrive(&sm.q_full[t]);
                 int seen = valid ? PromptWalk::limit(A, it.s, row) : 0x7fffffff;   // columns below it count
 
-                for (int j = 0; j < nt; ++j, seen -= kPromptTile) {
-                    bool ok = tc::bar_wait(&sm.s_full[t], mine & 1, abort, A.status);
+                for (int j = 0; j < nt; ++j, seen -= kPromptStep) {
+                    const int half = mine & 1;                          // of the score columns, in turn
+                    const uint32_t cols = s_addr + 64 * half;
+                    bool ok = tc::bar_wait(&sm.s_full[t][half], (mine >> 1) & 1, abort, A.status);
                     if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
                     tc::fence_after();
-                    const int slot = (done + j) & 7;
-                    // 64 columns at a time, and read twice (for the maximum and
-                    // for P): a read takes some 30 clocks, a spilled register
-                    // ten times that
                     uint32_t x[2][32];
-                    const auto columns = [&](int h) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) tc::tmem_load(s_addr + 64 * h + 32 * c, x[c]);
+                    for (int c = 0; c < 2; ++c) tc::tmem_load(cols + 32 * c, x[c]);
+                    const int slot = (done + (j >> 1)) & 7, quarter = 2 * (j & 1);
+                    float f[2], ev[2];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) tc::tmem_load_wait(x[c]);
-                        if (seen < 64 * (h + 1)) {
+                    for (int c = 0; c < 2; ++c) {
+                        // (above zero, so that a masked -inf stays -inf)
+                        f[c] = fmaxf(fac * sm.kf[slot][quarter + c], 1e-37f);
+                        ev[c] = sm.ve[slot][quarter + c];
+                    }
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c) tc::tmem_load_wait(x[c]);
+                    if (seen < 64) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (64 * h + 32 * c + i >= seen) x[c][i] = 0xFF800000u;
-                        }
-                    };
-                    // (above zero, so that a masked -inf stays -inf)
-                    const auto factor = [&](int c) { return fmaxf(fac * sm.kf[slot][c], 1e-37f); };
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i >= seen) x[c][i] = 0xFF800000u;
+                    }
                     // row maximum, each 32 positions with their factor and exponent
                     float want = -INFINITY;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        columns(h);
+                    for (int c = 0; c < 2; ++c) {
+                        float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                a = max3_nan(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-                                b = max3_nan(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
-                            }
-                            want = max_nan(want, fmaf(max_nan(a, b), factor(2 * h + c), sm.ve[slot][2 * h + c]));
+                        for (int i = 0; i < 32; i += 4) {
+                            a = max3_nan(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                            b = max3_nan(b, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
                         }
+                        want = max_nan(want, fmaf(max_nan(a, b), f[c], ev[c]));
                     }
                     // P is at most 2^7 when the maximum is new, 2^15 before it is raised
                     want -= 7.0f;
@@ -319,7 +327,7 @@ attend_prompt_kernel(const AttArgs A) {
                         m = now;
                         l *= alpha;
                         if (j > 0) {
-                            ok = tc::bar_wait(&sm.o_full[t], (mine - 1) & 1, abort, A.status);
+                            ok = summed();
                             if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
                             tc::fence_after();
 #pragma unroll 1
@@ -334,35 +342,31 @@ attend_prompt_kernel(const AttArgs A) {
                     }
                     const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        columns(h);
+                    for (int c = 0; c < 2; ++c) {
+                        const float off = ev[c] - mu;
+                        float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float f = factor(2 * h + c), off = sm.ve[slot][2 * h + c] - mu;
-                            float sum0 = 0.0f, sum1 = 0.0f;
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t p[8];                              // over columns already read
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                uint32_t p[8];                          // over columns already read
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float p0 = ex2(fmaf(__uint_as_float(x[c][16 * g + 2 * i]), f, off));
-                                    const float p1 = ex2(fmaf(__uint_as_float(x[c][16 * g + 2 * i + 1]), f, off));
-                                    sum0 += p0;
-                                    sum1 += p1;
-                                    p[i] = f16x2_rn(p0, p1);
-                                }
-                                tc::tmem_store8(s_addr + 32 * h + 16 * c + 8 * g, p);
+                            for (int i = 0; i < 8; ++i) {
+                                const float p0 = ex2(fmaf(__uint_as_float(x[c][16 * g + 2 * i]), f[c], off));
+                                const float p1 = ex2(fmaf(__uint_as_float(x[c][16 * g + 2 * i + 1]), f[c], off));
+                                sum0 += p0;
+                                sum1 += p1;
+                                p[i] = f16x2_rn(p0, p1);
                             }
-                            l = fmaf(sum0 + sum1, sm.vi[slot][2 * h + c], l);
+                            tc::tmem_store8(cols + 16 * c + 8 * g, p);
                         }
+                        l = fmaf(sum0 + sum1, sm.vi[slot][quarter + c], l);
                     }
                     tc::tmem_store_wait();
                     tc::fence_before();
-                    tc::bar_arrive(&sm.p_full[t]);
+                    tc::bar_arrive(&sm.p_full[t][half]);
                     ++mine;
                 }
                 if (!live) break;
-                const bool ok = tc::bar_wait(&sm.o_full[t], (mine - 1) & 1, abort, A.status);
+                const bool ok = summed();
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::fence_after();
             }
@@ -449,80 +453,77 @@ attend_prompt_kernel(const AttArgs A) {
         }
     } else {
         // ---------------- MMA issue ----------------
-        constexpr uint32_t id_s = tc::idesc_f16(128, 128, false), id_o = tc::idesc_f16(128, D, true);
-        int done = 0;
-        uint32_t phases = 0;                         // bit t: of p_full[t]; bit 2 + t: of q_full[t]
+        constexpr uint32_t id_s = tc::idesc_f16(128, 64, false), id_o = tc::idesc_f16(128, D, true);
+        const int t = warp - 12;
+        int done = 0, mine = 0;                      // position tiles of the CTA, steps of this row tile so far
+        uint32_t q_phase = 0;
         bool live = true;
         const auto wait = [&](uint64_t *bar, int phase) {
             live = live && __all_sync(0xffffffffu, tc::bar_wait(bar, phase & 1, abort, A.status));
         };
-        constexpr uint32_t kStep = 128 * D * 2 / 16;                 // one tile, in descriptor units
-        const uint64_t q_desc = tc::desc_k_major(tc::smem_addr(sm.q[0])), k_desc = tc::desc_k_major(tc::smem_addr(sm.k[0]));
+        constexpr uint32_t kStage = 128 * D * 2 / 16;                // one tile, in descriptor units
+        const uint64_t q_desc = tc::desc_k_major(tc::smem_addr(sm.q[t])), k_desc = tc::desc_k_major(tc::smem_addr(sm.k[0]));
         const uint64_t v_desc = tc::desc_n_major(tc::smem_addr(sm.v[0]), 16384);
-        // O += P V for the values of stage sv, S = Q K^T for the keys of stage
-        // sk (loops, so that no table of descriptors is kept in registers)
-        const auto issue = [&](int t, bool sums, int sv, bool more, bool scores, int sk) {
-            if (tc::elect()) {
-                if (sums) {
-                    uint64_t b = v_desc + sv * kStep;
-                    uint32_t p = tmem + 128 * t;
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h, b += 4 * 128, p += 32) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_ts(tmem + 256 + D * t, p + 8 * kk, b + 128 * kk, id_o, more || h + kk != 0);
-                    }
-                    tc::commit(&sm.o_full[t]);
-                }
-                if (scores) {
-                    uint64_t a = q_desc + t * kStep, b = k_desc + sk * kStep;
+        const uint32_t s_col = tmem + 128 * t, o_col = tmem + 256 + D * t;
+        while (live && sm.walk[warp].next(A, false)) {
+            const int steps = it.steps, nt = it.nt[t];
+            // S = Q K^T of step i (64 positions) into its half of the columns
+            const auto scores = [&](int i) {
+                const int n = done + (i >> 1);
+                if (!(i & 1)) wait(&sm.k_full[n & 1], n >> 1);
+                if (live && tc::elect()) {
+                    uint64_t a = q_desc, b = k_desc + (n & 1) * kStage + (i & 1) * 512;
+                    const uint32_t d = s_col + 64 * ((mine + i) & 1);
 #pragma unroll 1
                     for (int h = 0; h < D / 64; ++h, a += 1024, b += 1024) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_ss(tmem + 128 * t, a + 2 * kk, b + 2 * kk, id_s, h + kk != 0);
+                        for (int kk = 0; kk < 4; ++kk) tc::mma_ss(d, a + 2 * kk, b + 2 * kk, id_s, h + kk != 0);
                     }
-                    tc::commit(&sm.s_full[t]);
-                }
-            }
-            __syncwarp();
-        };
-        while (live && sm.walk[warp].next(A, false)) {
-            const int steps = it.steps, nt0 = it.nt[0], nt1 = it.nt[1];
-            for (int j = -1; j < steps && live; ++j) {
-                const int n = done + j;                              // of the values; the keys are one ahead
-                // both tiles are ready long before the rows are
-                if (j >= 0) wait(&sm.v_full[n & 1], n >> 1);
-                if (j + 1 < steps) wait(&sm.k_full[(n + 1) & 1], (n + 1) >> 1);
-#pragma unroll 1
-                for (int t = 0; t < 2; ++t) {
-                    const int nt = t ? nt1 : nt0;
-                    const bool sums = j >= 0 && j < nt, scores = j + 1 < nt;
-                    if (sums) {
-                        wait(&sm.p_full[t], phases >> t);
-                        phases ^= 1u << t;
-                    } else if (scores) {
-                        wait(&sm.q_full[t], phases >> (2 + t));
-                        phases ^= 4u << t;
-                    }
-                    if (live && (sums || scores)) {
-                        tc::fence_after();
-                        issue(t, sums, n & 1, j > 0, scores, (n + 1) & 1);
-                    }
-                }
-                if (live && tc::elect()) {
-                    if (j >= 0) tc::commit(&sm.v_empty[n & 1]);
-                    if (j + 1 < steps) tc::commit(&sm.k_empty[(n + 1) & 1]);
+                    tc::commit(&sm.s_full[t][(mine + i) & 1]);
+                    if ((i & 1) || i + 1 == nt) tc::commit(&sm.k_empty[n & 1]);
                 }
                 __syncwarp();
+            };
+            if (nt > 0) {
+                wait(&sm.q_full[t], q_phase);
+                q_phase ^= 1;
+                tc::fence_after();
+                scores(0);
+                if (nt > 1) scores(1);
             }
+            for (int i = 0; i < nt && live; ++i) {
+                // O += P V of step i, then the scores two steps ahead, over P
+                const int n = done + (i >> 1), half = (mine + i) & 1;
+                if (!(i & 1)) wait(&sm.v_full[n & 1], n >> 1);
+                wait(&sm.p_full[t][half], (mine + i) >> 1);
+                tc::fence_after();
+                if (live && tc::elect()) {
+                    const uint64_t b = v_desc + (n & 1) * kStage + (i & 1) * 512;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_ts(o_col, s_col + 64 * half + 8 * kk, b + 128 * kk, id_o, i > 0 || kk > 0);
+                    tc::commit(&sm.o_full[t][half]);
+                    if ((i & 1) || i + 1 == nt) tc::commit(&sm.v_empty[n & 1]);
+                }
+                __syncwarp();
+                if (live && i + 2 < nt) scores(i + 2);
+            }
+            // tiles that only the other row tile needs
+            for (int j = (nt + 1) / 2; j < steps && live; ++j) {
+                const int n = done + j;
+                wait(&sm.k_full[n & 1], n >> 1);
+                if (live && lane == 0) tc::bar_arrive(&sm.k_empty[n & 1]);
+                wait(&sm.v_full[n & 1], n >> 1);
+                if (live && lane == 0) tc::bar_arrive(&sm.v_empty[n & 1]);
+            }
+            mine += nt;
             done += steps;
         }
         // after an abort, products may still be running on this CTA's memory
-        if (tc::elect()) tc::commit(&sm.drained);
+        if (tc::elect()) tc::commit(&sm.drained[t]);
         __syncwarp();
         const uint64_t t0 = tc::now_ns();
-        while (!tc::bar_test(tc::smem_addr(&sm.drained), 0) && tc::now_ns() - t0 <= tc::kWaitLimitNs) {
+        while (!tc::bar_test(tc::smem_addr(&sm.drained[t]), 0) && tc::now_ns() - t0 <= tc::kWaitLimitNs) {
         }
         __syncwarp();
     }
