@@ -12,11 +12,12 @@
 //                accumulation per group of G channels, then one multiply-add
 //                with the group's scale.
 //  O^T = V^T P^T A = 16 channels x 16 tokens of codes as fp16, B = the
-//                probabilities times the tokens' group scales, fp16.  The
-//                power of two of a tile's largest value scale is part of the
-//                running maximum (p s lies in [0, 2^15)), so fp16's range of
-//                2^39 below it holds the rest: rounding 2^-12 per term,
-//                below the output type's own 2^-9.
+//                probabilities times the tokens' group scales, fp16 both and
+//                their product.  With 2^E the largest value scale of a tile,
+//                scales enter as s 2^(7 - E), probabilities as p 2^(E + 7)
+//                against a running maximum that holds E, so the products
+//                stay below 2^15 and what lies 2^-29 below the largest is
+//                lost; roundings 2^-12 each, below the output type's 2^-9.
 //
 // A query row is one (token, head of the group) pair, so the g heads of a
 // group share every code.  The probabilities pass from the layout of the
@@ -47,9 +48,13 @@ constexpr int kAttRowsMax = 16;
 // What CTA i leaves for the joining kernel: the segment that starts (and
 // does not end) in its share.
 struct AttMeta {
-    long long end;          // global number of the segment's last unit, plus 1
     long long units;        // units of the whole batch
-    int seq, seg;           // seq < 0: nothing to join
+    int last;               // the last share with a piece of the segment
+    int rows;               // of the segment; 0: nothing to join
+    int row0;               // its first row in the sequence
+    int head;
+    int token0;             // the sequence's first token row
+    int pad;
 };
 
 struct AttArgs {
@@ -60,6 +65,7 @@ struct AttArgs {
     int64_t tokens;
     int group;              // query heads per cache head
     float scale_log2;       // scale * log2(e)
+    uint32_t k16;           // 16
     int causal;
     dq_kv_cache cache;
     dq_kv_batch batch;
@@ -132,21 +138,25 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
 }
+__device__ __forceinline__ uint32_t mul_lo(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.lo.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 // (x & m) | (y & ~m)
 __device__ __forceinline__ uint32_t bit_select(uint32_t x, uint32_t y, uint32_t m) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(x), "r"(y), "r"(m));
     return r;
 }
-// (x & m) | v
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t v) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(v));
-    return r;
-}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -155,15 +165,21 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// (x & m) ^ v
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t m, uint32_t v) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "r"(m), "r"(v));
+    return r;
+}
 // Eight INT4 codes of a word: out[i] holds nibbles i (low) and i + 4 (high)
 // as fp16.  With u = c + 8, 0x6400 | u is 1024 + u; for the nibbles in bits 4
 // to 7 it is 1024 + 16 u, brought down by a multiply-add; all exact.
 __device__ __forceinline__ void int4_halves(uint32_t w, uint32_t (&out)[4]) {
-    const uint32_t u = w ^ 0x88888888u, u8 = u >> 8;
-    out[0] = hsub2(and_or(u, 0x000F000Fu, 0x64006400u), 0x64086408u);
-    out[1] = hfma2(and_or(u, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);   // / 16, - 72
-    out[2] = hsub2(and_or(u8, 0x000F000Fu, 0x64006400u), 0x64086408u);
-    out[3] = hfma2(and_or(u8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);
+    const uint32_t w8 = w >> 8;
+    out[0] = hsub2(and_xor(w, 0x000F000Fu, 0x64086408u), 0x64086408u);
+    out[1] = hfma2(and_xor(w, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);   // / 16, - 72
+    out[2] = hsub2(and_xor(w8, 0x000F000Fu, 0x64086408u), 0x64086408u);
+    out[3] = hfma2(and_xor(w8, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);
 }
 // Eight E2M1 codes of a word by bytes: out[i] holds nibbles 2i (low) and 2i + 1.
 __device__ __forceinline__ void e2m1_bytes(uint32_t w, uint32_t (&out)[4]) {
@@ -174,17 +190,22 @@ __device__ __forceinline__ void e2m1_bytes(uint32_t w, uint32_t (&out)[4]) {
 }
 // Two halves of 4 nibbles each (a token each): out[i] holds nibble i of the
 // low half and nibble i of the high half.
+// (k16: 16, a value the compiler does not know)
 template <int CODES>
-__device__ __forceinline__ void nibble_pairs(uint32_t x, uint32_t (&out)[4]) {
+__device__ __forceinline__ void nibble_pairs(uint32_t x, uint32_t (&out)[4], uint32_t k16) {
     if constexpr (CODES == CODES_INT4) {
         int4_halves(x, out);
     } else {
-        const uint32_t z = bit_select(x, x >> 12, 0x0F0F0F0Fu);      // bytes 0, 1: nibbles 0, 2
-        const uint32_t w = bit_select(x >> 4, x >> 16, 0x0F0F0F0Fu); // bytes 0, 1: nibbles 1, 3
-        asm("{ .reg .b8 p, q, r, s, t; mov.b32 {p, q, t, t}, %4; mov.b32 {r, s, t, t}, %5;\n\t"
+        // bytes 2 and 3 of e: nibbles 0, 2; of o: nibbles 1, 3 (the second
+        // token's in the upper half).  The shifts go to the left and are
+        // multiplications: the kernel is bound by the pipe of logic, shifts
+        // and conversions, not by that of the multipliers.
+        const uint32_t e = bit_select(mul_lo(x, k16), mul_lo(x, k16 * 4096u), 0xF0F0F0F0u);
+        const uint32_t o = bit_select(x, mul_lo(x, k16 * 256u), 0xF0F0F0F0u);
+        asm("{ .reg .b8 p, q, r, s, t; mov.b32 {t, t, p, q}, %4; mov.b32 {t, t, r, s}, %5;\n\t"
             "cvt.rn.f16x2.e2m1x2 %0, p; cvt.rn.f16x2.e2m1x2 %2, q;\n\t"
             "cvt.rn.f16x2.e2m1x2 %1, r; cvt.rn.f16x2.e2m1x2 %3, s; }"
-            : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3]) : "r"(z), "r"(w));
+            : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3]) : "r"(e), "r"(o));
     }
 }
 
@@ -258,13 +279,15 @@ struct AttShape {
     static constexpr int CB = kAttTile * D / 2;                  // code bytes of a warp tile
     static constexpr int TB = kAttTile * SB;                     // scale bytes of a warp tile
     static constexpr int STAGE = 2 * CB + 2 * TB;
-    static constexpr int RING_MAX = 108 * 1024 / kAttWarps / STAGE;
+    // a warp tile's scales by group and token: values' as fp16, keys' as float32
+    static constexpr int VS_BYTES = NG * kAttTile * 6;
+    static constexpr int RING_MAX = (112 * 1024 / kAttWarps - VS_BYTES - 64 * NB) / STAGE;
     static constexpr int RING = RING_MAX > 5 ? 5 : RING_MAX;
     static constexpr int RING_BYTES = kAttWarps * RING * STAGE;
     static constexpr int OST = D + 4;                            // row stride of the joining buffer
     static constexpr int JOIN_BYTES = kAttWarps * ROWS * OST * 4;
     static constexpr int BODY = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
-    static constexpr int BYTES = BODY + kAttWarps * ROWS * 8 + 64;
+    static constexpr int BYTES = BODY + kAttWarps * (ROWS * 8 + VS_BYTES);
     static_assert(RING >= 2, "ring");
 };
 
@@ -325,10 +348,8 @@ attend_split_kernel(const AttArgs A) {
     const long long u0 = units * me / n, u1 = units * (me + 1) / n;
     if (tid == 0) {
         AttMeta m;
-        m.end = 0;
         m.units = units;
-        m.seq = -1;
-        m.seg = 0;
+        m.last = m.rows = m.row0 = m.head = m.token0 = m.pad = 0;
         A.meta[me] = m;
     }
     if (u0 >= u1) return;
@@ -357,6 +378,9 @@ attend_split_kernel(const AttArgs A) {
     long long first = s_first;
 
     uint8_t *const ring = att_smem_raw + warp * RING * Sh::STAGE;
+    uint16_t *const vs16 = reinterpret_cast<uint16_t *>(att_smem_raw + Sh::BODY + kAttWarps * ROWS * 8) +
+                           warp * (Sh::VS_BYTES / 2);
+    float *const ks32 = reinterpret_cast<float *>(vs16 + Sh::NG * kAttTile);
     const uint32_t ring_s = att_smem(ring);
     // byte of this lane's row in a matrix load: token (lane & 7) + 8 of matrix 1, 3; chunk + 1 of 2, 3
     const int lm_t = (lane & 7) + ((lane >> 3) & 1) * 8, lm_c = lane >> 4;
@@ -383,6 +407,69 @@ attend_split_kernel(const AttArgs A) {
         const int lim_min = limit(row0), lim_max = limit(row0 + rows - 1);
         const int lo = t0 * kAttUnit, hi = min(t1 * kAttUnit, lim_max);
 
+        // ---- tokens, 32 at a time; the first loads go out before anything else
+        const int base0 = lo + kAttTile * warp;
+        const int nt = hi > base0 ? (hi - base0 + kAttUnit - 1) / kAttUnit : 0;
+        // a tile is two runs of 16 tokens, each inside a page; lane 0 (16) and
+        // its neighbours follow the first (second): its page and slot, tile by tile
+        const int ps = A.cache.page_size, hop_pages = kAttUnit / ps, hop_slots = kAttUnit - hop_pages * ps;
+        const int32_t *const table = A.batch.block_table + seq * A.batch.table_stride;
+        int at_pos = base0 + (lane & 16), at_page = at_pos / ps, at_slot = at_pos - at_page * ps;
+        // row in the cache of this lane's run of the next tile, or -1
+        const auto next_row = [&]() -> int64_t {
+            int64_t row = -1;
+            if (at_pos < hi) {
+                const int page = __ldg(table + at_page);
+                if (page >= 0 && (int64_t)page < A.cache.pages) row = ((int64_t)page * heads + head) * ps + at_slot;
+                else atomicOr(A.status, STATUS_INDEX);
+            }
+            at_pos += kAttUnit;
+            at_page += hop_pages;
+            at_slot += hop_slots;
+            if (at_slot >= ps) at_slot -= ps, ++at_page;
+            return row;
+        };
+        const auto issue = [&](int i, int64_t row) {
+            if (i < nt) {
+                const uint32_t st = ring_s + (i % RING) * Sh::STAGE;
+                const int64_t row_a = __shfl_sync(0xffffffffu, row, 0), row_b = __shfl_sync(0xffffffffu, row, 16);
+                // codes: 16 bytes per lane and step, in the order of the rows
+                constexpr int CPR = D / 32;                     // 16-byte chunks per code row
+                const uint32_t dst = st + code_off<D>(lane / CPR, lane % CPR);
+                const bool ok_a = row_a >= 0, ok_b = row_b >= 0;
+                const int64_t off_a = (ok_a ? row_a * (D / 2) : 0) + lane * 16;
+                const int64_t off_b = (ok_b ? row_b * (D / 2) : 0) + lane * 16;
+                const uint8_t *const ka = A.cache.k_codes + off_a, *const kb = A.cache.k_codes + off_b;
+                const uint8_t *const va = A.cache.v_codes + off_a, *const vb = A.cache.v_codes + off_b;
+#pragma unroll
+                for (int k = 0; k < CPR / 2; ++k) {             // (nothing is read where !ok)
+                    cp16(dst + k * 512, ka + k * 512, ok_a);
+                    cp16(dst + (k + CPR / 2) * 512, kb + k * 512, ok_b);
+                    cp16(dst + k * 512 + Sh::CB, va + k * 512, ok_a);
+                    cp16(dst + (k + CPR / 2) * 512 + Sh::CB, vb + k * 512, ok_b);
+                }
+                // scales: SB chunks of 16 bytes per run, keys then values
+#pragma unroll
+                for (int k = 0; k < (4 * Sh::SB + 31) / 32; ++k) {
+                    const int x = k * 32 + lane;
+                    if (4 * Sh::SB % 32 == 0 || x < 4 * Sh::SB) {
+                        const int64_t row = (x / Sh::SB) % 2 ? row_b : row_a;
+                        cp16(st + 2 * Sh::CB + x * 16,
+                             reinterpret_cast<const uint8_t *>(x < 2 * Sh::SB ? A.cache.k_scales : A.cache.v_scales) +
+                                 (row < 0 ? 0 : row * Sh::SB + (x % Sh::SB) * 16),
+                             row >= 0);
+                    }
+                }
+            }
+            cp_commit();
+        };
+        int64_t row_next = next_row();
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) {
+            const int64_t row = row_next;
+            row_next = next_row();
+            issue(i, row);
+        }
         // ---- the query rows: B operands, and the factor that takes a
         // product of scaled operands to log2 units
         uint32_t qf[NB][NJ][4];
@@ -448,56 +535,10 @@ attend_split_kernel(const AttArgs A) {
             m[nb][0] = m[nb][1] = -INFINITY;
             l[nb][0] = l[nb][1] = 0.0f;
         }
-        // ---- tokens, 32 at a time
-        const int base0 = lo + kAttTile * warp;
-        const int nt = hi > base0 ? (hi - base0 + kAttUnit - 1) / kAttUnit : 0;
-        // this lane's token of tile i: its row in the cache, or -1
-        const auto row_of = [&](int i) -> int64_t {
-            const int pos = base0 + i * kAttUnit + lane;
-            if (i >= nt || pos >= hi) return -1;
-            const int64_t row = kv_row(A.cache, A.batch, seq, pos, head);
-            if (row < 0) atomicOr(A.status, STATUS_INDEX);
-            return row;
-        };
-        const auto issue = [&](int i, int64_t row) {
-            if (i < nt) {
-                const uint32_t st = ring_s + (i % RING) * Sh::STAGE;
-                constexpr int CPR = D / 32;                     // 16-byte chunks per code row
-#pragma unroll
-                for (int k = 0; k < CPR; ++k) {
-                    const int t = (k * 32 + lane) / CPR, ch = (k * 32 + lane) % CPR;
-                    const int64_t rw = __shfl_sync(0xffffffffu, row, t);
-                    const int64_t off = rw < 0 ? 0 : rw * (D / 2) + ch * 16;
-                    const uint32_t d = st + code_off<D>(t, ch);
-                    cp16(d, A.cache.k_codes + off, rw >= 0);
-                    cp16(d + Sh::CB, A.cache.v_codes + off, rw >= 0);
-                }
-                // scales: chunks of 16 bytes, 16 / SB consecutive tokens of one page
-                constexpr int CH = kAttTile * Sh::SB / 16;
-#pragma unroll
-                for (int k = 0; k < (2 * CH + 31) / 32; ++k) {
-                    const int x = k * 32 + lane, ch = x % CH;
-                    const int64_t rw = __shfl_sync(0xffffffffu, row, ch * 16 / Sh::SB);
-                    if (x < 2 * CH)
-                        cp16(st + 2 * Sh::CB + (x / CH) * Sh::TB + ch * 16,
-                             reinterpret_cast<const uint8_t *>(x < CH ? A.cache.k_scales : A.cache.v_scales) +
-                                 (rw < 0 ? 0 : rw * Sh::SB),
-                             rw >= 0);
-                }
-            }
-            cp_commit();
-        };
-        int64_t row_next = row_of(0);
-#pragma unroll
-        for (int i = 0; i < RING - 1; ++i) {
-            const int64_t row = row_next;
-            row_next = row_of(i + 1);
-            issue(i, row);
-        }
         for (int it = 0; it < nt; ++it) {
             {
                 const int64_t row = row_next;
-                row_next = row_of(it + RING);
+                row_next = next_row();
                 issue(it + RING - 1, row);
             }
             cp_wait<RING - 1>();
@@ -506,24 +547,35 @@ attend_split_kernel(const AttArgs A) {
             const uint32_t st_s = ring_s + (it % RING) * Sh::STAGE;
             uint8_t *const ks = st + 2 * Sh::CB, *const vs = ks + Sh::TB;
             const int base = base0 + it * kAttUnit;
-            // value scales of tokens that no row sees count as zero
-            if (base + kAttTile > hi) {
-                if (base + lane >= hi) Sw::zero(vs + lane * Sh::SB);
-                __syncwarp();
-            }
-            int ev;                                             // exponent of the tile's largest value scale
+            // scales, token by token: keys' as float32, values' as fp16
+            // relative to the largest; values' of tokens that no row sees are
+            // zero
+            int ev;                                             // its exponent
             {
                 Sw v;
                 v.load(vs + lane * Sh::SB);
+                if (base + lane >= hi) {
+#pragma unroll
+                    for (int i = 0; i < Sw::N; ++i) v.w[i] = 0;
+                }
                 ev = max(__reduce_max_sync(0xffffffffu, v.template top<GS>()), -90);
+                const float down = pow2f(7 - ev);
+#pragma unroll
+                for (int g = 0; g < Sh::NG; ++g) {
+                    const uint32_t h = f16x2_rn(v.template get<GS>(g) * down, 0.0f);
+                    vs16[g * kAttTile + lane] = (uint16_t)h;
+                }
+                Sw k;
+                k.load(ks + lane * Sh::SB);
+#pragma unroll
+                for (int g = 0; g < Sh::NG; ++g) ks32[g * kAttTile + lane] = k.template get<GS>(g);
+                __syncwarp();
             }
             // ---- scores
             float sc[2][NB][4];
 #pragma unroll
             for (int mb = 0; mb < 2; ++mb) {
-                Sw k0, k8;
-                k0.load(ks + (mb * 16 + r) * Sh::SB);
-                k8.load(ks + (mb * 16 + r + 8) * Sh::SB);
+                const float *const sk = ks32 + mb * 16 + r;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -551,11 +603,11 @@ attend_split_kernel(const AttArgs A) {
 #pragma unroll
                                 for (int half = 0; half < 2; ++half) {
                                     const bool on = (c >> 1) == half;
+                                    const int g = 2 * (j + jj) + half;
                                     float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                                     mma_f16(d, x[0], y[0], x[1], y[1], on ? q[0] : 0u, on ? q[1] : 0u);
                                     mma_f16(d, x[2], y[2], x[3], y[3], on ? q[2] : 0u, on ? q[3] : 0u);
-                                    const int g = 2 * (j + jj) + half;
-                                    const float s0 = k0.template get<GS>(g), s8 = k8.template get<GS>(g);
+                                    const float s0 = sk[g * kAttTile], s8 = sk[g * kAttTile + 8];
                                     sc[mb][nb][0] = fmaf(d[0], s0, sc[mb][nb][0]);
                                     sc[mb][nb][1] = fmaf(d[1], s0, sc[mb][nb][1]);
                                     sc[mb][nb][2] = fmaf(d[2], s8, sc[mb][nb][2]);
@@ -570,7 +622,7 @@ attend_split_kernel(const AttArgs A) {
                                 mma_f16(acc[nb], x[2], y[2], x[3], y[3], q[2], q[3]);
                                 if (G == 32 || jj == 1) {
                                     const int g = (j + jj) * 32 / G;
-                                    const float s0 = k0.template get<GS>(g), s8 = k8.template get<GS>(g);
+                                    const float s0 = sk[g * kAttTile], s8 = sk[g * kAttTile + 8];
                                     sc[mb][nb][0] = fmaf(acc[nb][0], s0, sc[mb][nb][0]);
                                     sc[mb][nb][1] = fmaf(acc[nb][1], s0, sc[mb][nb][1]);
                                     sc[mb][nb][2] = fmaf(acc[nb][2], s8, sc[mb][nb][2]);
@@ -582,8 +634,8 @@ attend_split_kernel(const AttArgs A) {
                 }
             }
             // ---- softmax: the running maximum carries the exponent of the
-            // tile's value scales, so that p s stays below 2^15 (m is at
-            // least the largest score + exponent - 14 of every tile)
+            // tiles' value scales (m is at least the largest score + exponent
+            // - 7 of every tile), p 2^E is what the products take
             const bool cut = base + kAttTile > lim_min;
             bool moved = false;
             float alpha[NB][2], mu[NB][2];
@@ -612,7 +664,7 @@ attend_split_kernel(const AttArgs A) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float old = m[nb][h];
-                    const float now = max_nan(old, alpha[nb][h] + (float)(ev - 14));
+                    const float now = max_nan(old, alpha[nb][h] + (float)(ev - 7));
                     m[nb][h] = now;
                     mu[nb][h] = now == -INFINITY ? 0.0f : now;
                     alpha[nb][h] = ex2(old - mu[nb][h]);
@@ -629,29 +681,36 @@ attend_split_kernel(const AttArgs A) {
                         for (int k = 0; k < 8; ++k) o[nb][j][k >> 2][k & 3] *= alpha[nb][k & 1];
                 }
             }
+            uint32_t pt[2][NB][2];                              // transposed: tokens 2c, 2c + 1 (+ 8) of row r
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb) {
+                float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int mb = 0; mb < 2; ++mb)
+                for (int mb = 0; mb < 2; ++mb) {
+                    float p[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float p = ex2(sc[mb][nb][k] - mu[nb][k & 1]);
-                        sc[mb][nb][k] = p;
-                        l[nb][k & 1] += p;
+                        p[k] = ex2(sc[mb][nb][k] - (mu[nb][k & 1] - (float)ev));
+                        sum[k & 1] += p[k];
                     }
+                    pt[mb][nb][0] = movm(f16x2_rn(p[0], p[1]));
+                    pt[mb][nb][1] = movm(f16x2_rn(p[2], p[3]));
+                }
+                const float up = pow2f(7 - ev);                 // (as the scales)
+                l[nb][0] = fmaf(sum[0], up, l[nb][0]);
+                l[nb][1] = fmaf(sum[1], up, l[nb][1]);
+            }
             // ---- values
 #pragma unroll
             for (int mb = 0; mb < 2; ++mb) {
-                Sw v0, v8;
-                v0.load(vs + (mb * 16 + r) * Sh::SB);
-                v8.load(vs + (mb * 16 + r + 8) * Sh::SB);
                 uint32_t p0[NB], p1[NB], p2[NB], p3[NB];        // B operands of the group(s) at hand
                 const auto probs = [&](int g, uint32_t(&b0)[NB], uint32_t(&b1)[NB]) {
-                    const float s0 = v0.template get<GS>(g), s8 = v8.template get<GS>(g);
+                    const uint32_t *const s2 = reinterpret_cast<const uint32_t *>(vs16 + g * kAttTile + mb * 16);
+                    const uint32_t s0 = s2[c], s8 = s2[c + 4];
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
-                        b0[nb] = movm(f16x2_rn(sc[mb][nb][0] * s0, sc[mb][nb][1] * s0));
-                        b1[nb] = movm(f16x2_rn(sc[mb][nb][2] * s8, sc[mb][nb][3] * s8));
+                        b0[nb] = hmul2(pt[mb][nb][0], s0);
+                        b1[nb] = hmul2(pt[mb][nb][1], s8);
                     }
                 };
 #pragma unroll
@@ -677,8 +736,8 @@ attend_split_kernel(const AttArgs A) {
                             probs((j + jj) * 32 / G, p0, p1);
                         }
                         uint32_t x[4], y[4];
-                        nibble_pairs<CODES>(wa, x);
-                        nibble_pairs<CODES>(wb, y);
+                        nibble_pairs<CODES>(wa, x, A.k16);
+                        nibble_pairs<CODES>(wb, y, A.k16);
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
                             mma_f16(o[nb][j + jj][0], x[0], x[1], y[0], y[1], p0[nb], p1[nb]);
@@ -757,11 +816,15 @@ attend_split_kernel(const AttArgs A) {
             }
         }
         if (!whole && t0 == 0 && tid == 0) {
+            const long long end = first + (long long)(seg + 1) * sp.kvt;    // (its last unit, plus 1)
             AttMeta mt;
-            mt.end = first + (long long)(seg + 1) * sp.kvt;
             mt.units = units;
-            mt.seq = seq;
-            mt.seg = seg;
+            mt.last = (int)min((long long)n - 1, (end * n - 1) / units);
+            mt.rows = rows;
+            mt.row0 = row0;
+            mt.head = head;
+            mt.token0 = s.s0;
+            mt.pad = 0;
             A.meta[me] = mt;
         }
         __syncthreads();
@@ -780,15 +843,10 @@ attend_join_kernel(const AttArgs A, int n) {
     __shared__ float4 s_acc[4][D / 4];
     __shared__ float s_sum[4];
     const AttMeta mt = A.meta[blockIdx.x];
-    if (mt.seq < 0) return;
     const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, mt.seq);
-    const AttSpan sp = att_span<ROWS>(s, A.group, A.cache.heads);
-    const int head = mt.seg / sp.qt, rr = (mt.seg - head * sp.qt) * ROWS + row;
-    if (rr >= s.n * A.group) return;
+    if (row >= mt.rows) return;
     // shares i, i + 1, ..., last hold pieces (empty shares hold none)
-    const int i0 = blockIdx.x;
-    const int last = (int)min((long long)n - 1, (mt.end * n - 1) / mt.units);
+    const int i0 = blockIdx.x, last = mt.last;
     const auto piece = [&](int i) {             // slot, or -1
         if (mt.units < n && i > i0 && mt.units * i / n >= mt.units * (i + 1) / n) return -1;
         return 2 * i + (i == i0 ? 1 : 0);
@@ -832,12 +890,12 @@ attend_join_kernel(const AttArgs A, int n) {
         sum += s_sum[w];
     }
     const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
-    const int tok = rr / A.group;
+    const int rr = mt.row0 + row, tok = rr / A.group;
     uint2 v;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(acc.y * inv), "f"(acc.x * inv));
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(acc.w * inv), "f"(acc.z * inv));
-    *reinterpret_cast<uint2 *>(A.out + (s.s0 + tok) * A.out_token +
-                               (int64_t)(head * A.group + rr - tok * A.group) * A.out_head + 4 * lane) = v;
+    *reinterpret_cast<uint2 *>(A.out + (mt.token0 + tok) * A.out_token +
+                               (int64_t)(mt.head * A.group + rr - tok * A.group) * A.out_head + 4 * lane) = v;
 }
 
 // ---- launch
@@ -854,6 +912,7 @@ inline AttArgs att_args(const AttendLaunch &L, int rows) {
     A.group = L.q_heads / L.cache.heads;
     A.scale_log2 = L.scale * 1.44269504088896341f;
     A.causal = L.causal;
+    A.k16 = 16;
     A.cache = L.cache;
     A.batch = L.batch;
     uint8_t *w = static_cast<uint8_t *>(L.workspace);
@@ -876,6 +935,9 @@ cudaError_t launch_attend_split(AttendLaunch &L) {
     if (e != cudaSuccess) return e;
     e = launch_k(kern, dim3(kAttCtas), dim3(kAttThreads), Sh::BYTES, L.stream, A);
     if (e != cudaSuccess) return e;
+    L.launches = 1;
+    // (sequences of at most one unit are never cut)
+    if ((int64_t)L.batch.max_pages * L.cache.page_size <= kAttUnit) return cudaSuccess;
     L.launches = 2;
     return launch_k(attend_join_kernel<D, NB>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
 }

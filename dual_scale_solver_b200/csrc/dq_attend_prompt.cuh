@@ -150,12 +150,6 @@ __device__ __forceinline__ void prompt_scales(ScaleWords<SB> &s, const void *sca
     }
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // Expands a token's row into a tile, with scales relative to 2^e; the order of
 // the 8 elements of a chunk is the one the code conversion gives
 // (prompt_order).
