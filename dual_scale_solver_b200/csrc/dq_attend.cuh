@@ -463,13 +463,24 @@ attend_split_kernel(const AttArgs A) {
             }
             cp_commit();
         };
-        int64_t row_next = next_row();
+        // (every load that depends on nothing else first)
+        uint4 raw[NB][NJ];
 #pragma unroll
-        for (int i = 0; i < RING - 1; ++i) {
-            const int64_t row = row_next;
-            row_next = next_row();
-            issue(i, row);
+        for (int nb = 0; nb < NB; ++nb) {
+            const int row = row0 + 8 * nb + r, tok = row / A.group;
+            const uint16_t *p = A.q + (s.s0 + tok) * A.q_token +
+                                (int64_t)(head * A.group + row - tok * A.group) * A.q_head + 8 * c;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                raw[nb][j] = 8 * nb + r < rows ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * j)) : make_uint4(0, 0, 0, 0);
         }
+        int64_t first_rows[RING];
+#pragma unroll
+        for (int i = 0; i < RING; ++i) first_rows[i] = next_row();
+        int64_t row_next = first_rows[RING - 1];
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) issue(i, first_rows[i]);
+
         // ---- the query rows: B operands, and the factor that takes a
         // product of scaled operands to log2 units
         uint32_t qf[NB][NJ][4];
@@ -477,21 +488,10 @@ attend_split_kernel(const AttArgs A) {
         int lim[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int row = row0 + 8 * nb + r;
-            uint4 raw[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) raw[j] = make_uint4(0, 0, 0, 0);
-            if (8 * nb + r < rows) {
-                const int tok = row / A.group;
-                const uint16_t *p = A.q + (s.s0 + tok) * A.q_token +
-                                    (int64_t)(head * A.group + row - tok * A.group) * A.q_head + 8 * c;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(p + 32 * j));
-            }
             uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const uint32_t v[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+                const uint32_t v[4] = {raw[nb][j].x, raw[nb][j].y, raw[nb][j].z, raw[nb][j].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) top = __vmaxu2(top, v[k] & 0x7FFF7FFFu);
             }
@@ -502,7 +502,7 @@ attend_split_kernel(const AttArgs A) {
             const float up = pow2f(13 - e);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const uint32_t v[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+                const uint32_t v[4] = {raw[nb][j].x, raw[nb][j].y, raw[nb][j].z, raw[nb][j].w};
                 float x[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
