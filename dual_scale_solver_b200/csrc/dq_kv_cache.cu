@@ -60,61 +60,76 @@ kv_copy_kernel(const KvCopyArgs A) {
             if (!READ) continue;
         }
         const int rows = 2 * A.cache.heads;             // keys, then values
-        for (int r0 = part * RPW; r0 < rows; r0 += A.splits * RPW) {
-            const int r = r0 + lane / LPR;
-            const bool ok = r < rows;
-            const bool val = r >= A.cache.heads;
-            const int head = ok ? (val ? r - A.cache.heads : r) : 0;
+        // UN steps at a time, their loads first: a warp's rows are few, and
+        // one load after the other would leave the memory idle
+        constexpr int UN = 2;
+        const int hop = A.splits * RPW;
+        for (int r0 = part * RPW; r0 < rows; r0 += UN * hop) {
+            uint16_t *x[UN];
+            uint8_t *codes[UN];
+            void *scales[UN];
+            int64_t gi[UN];
+            bool ok[UN];
+            uint4 in[UN];
+            float sc[UN];
             const int c = lane % LPR;
-            uint16_t *const x = (val ? A.v + t * A.v_token + head * A.v_head
-                                     : A.k + t * A.k_token + head * A.k_head) + 8 * c;
-            uint8_t *const codes = val ? A.cache.v_codes : A.cache.k_codes;
-            void *const scales = val ? A.cache.v_scales : A.cache.k_scales;
-            const int64_t row = row0 + (int64_t)head * A.cache.page_size;
-            const int64_t gi = row * (D / G) + c / (G / 8);
-            if constexpr (READ) {
-                if (!ok) continue;
-                uint4 o = make_uint4(0, 0, 0, 0);
-                if (row0 >= 0) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + row * (D / 2) + 4 * c);
-                    const float s = scale_value<GS>(scales, gi);
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                const int r = r0 + i * hop + lane / LPR;
+                ok[i] = r < rows;
+                const bool val = r >= A.cache.heads;
+                const int head = ok[i] ? (val ? r - A.cache.heads : r) : 0;
+                x[i] = (val ? A.v + t * A.v_token + head * A.v_head : A.k + t * A.k_token + head * A.k_head) + 8 * c;
+                const int64_t row = row0 + (int64_t)head * A.cache.page_size;
+                codes[i] = (val ? A.cache.v_codes : A.cache.k_codes) + row * (D / 2) + 4 * c;
+                scales[i] = val ? A.cache.v_scales : A.cache.k_scales;
+                gi[i] = row * (D / G) + c / (G / 8);
+                in[i] = make_uint4(0, 0, 0, 0);
+                sc[i] = 0.0f;
+                if constexpr (READ) {
+                    if (ok[i] && row0 >= 0) {
+                        in[i].x = *reinterpret_cast<const uint32_t *>(codes[i]);
+                        sc[i] = scale_value<GS>(scales[i], gi[i]);
+                    }
+                } else {
+                    if (ok[i]) in[i] = __ldg(reinterpret_cast<const uint4 *>(x[i]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                if (r0 + i * hop >= rows) break;        // (the whole warp)
+                if constexpr (READ) {
                     uint32_t p[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t b = (w >> (8 * k)) & 0xFFu;
+                        const uint32_t b = (in[i].x >> (8 * k)) & 0xFFu;
                         const float2 v = CODES == CODES_INT4
                                              ? make_float2((float)((int)((b & 15u) ^ 8u) - 8),
                                                            (float)((int)((b >> 4) ^ 8u) - 8))
                                              : e2m1x2_to_f32(b);
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[k]) : "f"(v.y * s), "f"(v.x * s));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[k]) : "f"(v.y * sc[i]), "f"(v.x * sc[i]));
                     }
-                    o = make_uint4(p[0], p[1], p[2], p[3]);
-                }
-                *reinterpret_cast<uint4 *>(x) = o;
-            } else {
-                f2 z[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) z[k] = make_float2(0.0f, 0.0f);
-                if (ok) {
+                    if (ok[i]) *reinterpret_cast<uint4 *>(x[i]) = make_uint4(p[0], p[1], p[2], p[3]);
+                } else {
                     Chunk<Bf16Tag> ch;
-                    ch.load(x);
+                    ch.raw = in[i];
+                    f2 z[4], code[4];
                     ch.unpack2(z);
-                }
-                f2 code[4];
-                float s, s_eff;
-                uint32_t cw[2], mbits;
-                bool nonzero;
-                Quant<CODES, GS, SC_BF16, true, 4, G / 8>::template run<true>(
-                    z, z, 1.0f, 1.0f, z, 1.0f, 1.0f, A.status, code, s, s_eff, cw, nonzero, mbits);
-                if (!ok) continue;
-                *reinterpret_cast<uint32_t *>(codes + row * (D / 2) + 4 * c) = cw[0];
-                if (c % (G / 8) == 0) {
-                    if constexpr (GS == SC_BF16)
-                        reinterpret_cast<uint16_t *>(scales)[gi] = (uint16_t)(__float_as_uint(s) >> 16);
-                    else if constexpr (GS == SC_E8M0)
-                        reinterpret_cast<uint8_t *>(scales)[gi] = (uint8_t)(__float_as_uint(s) >> 23);
-                    else
-                        reinterpret_cast<uint8_t *>(scales)[gi] = (uint8_t)e4m3_bits(s);
+                    float s, s_eff;
+                    uint32_t cw[2], mbits;
+                    bool nonzero;
+                    Quant<CODES, GS, SC_BF16, true, 4, G / 8>::template run<true>(
+                        z, z, 1.0f, 1.0f, z, 1.0f, 1.0f, A.status, code, s, s_eff, cw, nonzero, mbits);
+                    if (!ok[i]) continue;
+                    *reinterpret_cast<uint32_t *>(codes[i]) = cw[0];
+                    if (c % (G / 8) == 0) {
+                        if constexpr (GS == SC_BF16)
+                            reinterpret_cast<uint16_t *>(scales[i])[gi[i]] = (uint16_t)(__float_as_uint(s) >> 16);
+                        else if constexpr (GS == SC_E8M0)
+                            reinterpret_cast<uint8_t *>(scales[i])[gi[i]] = (uint8_t)(__float_as_uint(s) >> 23);
+                        else
+                            reinterpret_cast<uint8_t *>(scales[i])[gi[i]] = (uint8_t)e4m3_bits(s);
+                    }
                 }
             }
         }
@@ -138,7 +153,7 @@ cudaError_t launch_fmt(const KvCopyLaunch &L) {
     int splits = 1;
     while (splits < steps && L.tokens * splits < 148 * 16) splits *= 2;
     A.splits = splits;
-    const int64_t blocks = std::min<int64_t>((L.tokens * splits + 7) / 8, 148 * 8);
+    const int64_t blocks = (L.tokens * splits + 7) / 8;
     const dim3 grid((unsigned)blocks), block(256);
 #define DQ_KV(GG, DD)                                                                           \
     if (L.group == GG && L.cache.head_dim == DD)                                                \
