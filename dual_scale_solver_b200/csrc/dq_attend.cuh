@@ -43,7 +43,12 @@ constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kAttTile = 32;                       // tokens per warp step
 constexpr int kAttUnit = kAttTile * kAttWarps;     // tokens per unit
 constexpr int kAttCtas = 2 * 148;
-constexpr int kAttRowsMax = 16;
+
+// Calls of more than 8 query rows (new tokens x heads of a group) per sequence
+// go to the tcgen05 kernel, which takes 256 rows at a time.
+inline bool attend_by_prompt(int64_t tokens, int32_t q_heads, int32_t heads, int32_t seqs) {
+    return tokens * (q_heads / heads) > 8 * (int64_t)seqs;
+}
 
 // What CTA i leaves for the joining kernel: the segment that starts (and
 // does not end) in its share.
@@ -900,7 +905,7 @@ attend_join_kernel(const AttArgs A, int n) {
 
 // ---- launch
 
-inline AttArgs att_args(const AttendLaunch &L, int rows) {
+inline AttArgs att_args(const AttendLaunch &L, int slots, int rows) {
     AttArgs A;
     A.q = static_cast<const uint16_t *>(L.q);
     A.q_token = L.q_token;
@@ -917,9 +922,9 @@ inline AttArgs att_args(const AttendLaunch &L, int rows) {
     A.batch = L.batch;
     uint8_t *w = static_cast<uint8_t *>(L.workspace);
     A.part = reinterpret_cast<float *>(w);
-    w += (size_t)2 * kAttCtas * rows * L.cache.head_dim * sizeof(float);
+    w += (size_t)slots * rows * L.cache.head_dim * sizeof(float);
     A.part_ml = reinterpret_cast<float2 *>(w);
-    w += (size_t)2 * kAttCtas * rows * sizeof(float2);
+    w += (size_t)slots * rows * sizeof(float2);
     A.meta = reinterpret_cast<AttMeta *>(w);
     A.status = L.status;
     return A;
@@ -928,7 +933,7 @@ inline AttArgs att_args(const AttendLaunch &L, int rows) {
 template <int CODES, int GS, int G, int D, int NB>
 cudaError_t launch_attend_split(AttendLaunch &L) {
     using Sh = AttShape<CODES, GS, G, D, NB>;
-    const AttArgs A = att_args(L, Sh::ROWS);
+    const AttArgs A = att_args(L, 2 * kAttCtas, Sh::ROWS);
     const auto kern = attend_split_kernel<CODES, GS, G, D, NB>;
     static std::atomic<bool> done[64];
     cudaError_t e = smem_opt_in(kern, Sh::BYTES, done);

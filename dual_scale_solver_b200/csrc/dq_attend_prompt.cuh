@@ -43,6 +43,9 @@ constexpr int kPromptRows = 256;                 // query rows of a CTA
 constexpr int kPromptTile = 128;                 // positions of a tile of keys or values
 constexpr int kPromptStep = 64;                  // positions of a step of the softmax
 constexpr int kPromptThreads = 448;
+constexpr int kPromptCtas = 148;
+constexpr int kPromptPlan = 1024;                // sequences that a split is planned for
+constexpr int kPromptJoin = 6;                   // position tiles that cutting items costs a CTA
 constexpr int kPromptK0 = 12;                    // fp16 code x scale: at most 7 * 2^13
 
 // Byte of 16-byte chunk c (8 elements) of a row in a tile of 128 rows.
@@ -50,21 +53,25 @@ __device__ __forceinline__ uint32_t prompt_off(int row, int c) {
     return (uint32_t)((c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
 
+// A piece of work: 256 query rows of a sequence and cache head over the
+// position tiles [t0, t1) of the `steps` that the rows see.
 struct PromptItem {
     KvSeq s;
     int seq, head, row0;
-    int rows[2], nt[2];                          // valid rows and steps of positions of each row tile
-    int steps;                                   // tiles of positions
+    int rows[2], nt[2];                          // valid rows and steps of 64 positions of each row tile
+    int steps, t0, t1;
 };
 
-// The CTA's items, one per step: a sequence's row tiles go from the last
-// (longest, when causal) to the first, all heads of each; rounds of the grid
-// run forwards and backwards in turn, so that long and short ones pair up.
+// A warp's way through the CTA's pieces.  Either whole items: a sequence's row
+// tiles from the last (longest, when causal) to the first, all heads of each;
+// rounds of the grid run forwards and backwards in turn, so that long and
+// short ones pair up.  Or (left >= 0) an equal share of all position tiles in
+// that order, its first and last item cut where need be.
 struct PromptWalk {
-    int seq, round;
-    long long first;
+    int seq, round, tile, head, t;
+    long long first, left;
     PromptItem it;
-    // The next item, for the whole warp whose walk this is (in shared memory,
+    // The next piece, for the whole warp whose walk this is (in shared memory,
     // worked out by one lane: registers are short elsewhere).
     __device__ __forceinline__ bool next(const AttArgs &A, bool report) {
         __syncwarp();
@@ -72,36 +79,73 @@ struct PromptWalk {
         __syncwarp();
         return it.seq >= 0;
     }
+    __device__ __forceinline__ static int tiles(const AttArgs &A, const KvSeq &s) {
+        return (int)(((long long)s.n * A.group + kPromptRows - 1) / kPromptRows);
+    }
+    // position tiles that row tile pair `tile` sees
+    __device__ __forceinline__ static int span(const AttArgs &A, const KvSeq &s, int tile) {
+        const int last = (int)min((long long)(tile + 1) * kPromptRows, (long long)s.n * A.group) - 1;
+        return (limit(A, s, last) + kPromptTile - 1) / kPromptTile;
+    }
+    __device__ __forceinline__ void fill(const AttArgs &A, const KvSeq &s, int tl, int hd) {
+        const int all = s.n * A.group;
+        it.s = s;
+        it.seq = seq;
+        it.head = hd;
+        it.row0 = tl * kPromptRows;
+        it.steps = 0;
+        for (int i = 0; i < 2; ++i) {
+            const int r0 = it.row0 + 128 * i;
+            it.rows[i] = min(max(all - r0, 0), 128);
+            it.nt[i] = it.rows[i] == 0 ? 0 : (limit(A, s, r0 + it.rows[i] - 1) + kPromptStep - 1) / kPromptStep;
+            it.steps = max(it.steps, (it.nt[i] + 1) / 2);
+        }
+        it.t0 = 0;
+        it.t1 = it.steps;
+    }
     __device__ __forceinline__ void step(const AttArgs &A, bool report) {
+        it.seq = -1;
+        if (left >= 0) {
+            while (left > 0 && seq < A.batch.seqs) {
+                const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
+                if (tile < 0) tile = tiles(A, s) - 1;          // a new sequence
+                if (tile < 0) {
+                    ++seq;
+                    continue;
+                }
+                fill(A, s, tile, head);
+                const int take = (int)min(left, (long long)max(it.steps, 1) - t);
+                it.t0 = t;
+                it.t1 = min(t + take, it.steps);
+                left -= take;
+                t += take;
+                if (t >= it.steps) {
+                    t = 0;
+                    if (++head == A.cache.heads) {
+                        head = 0;
+                        if (--tile < 0) ++seq;
+                    }
+                }
+                return;
+            }
+            return;
+        }
         const long long n = gridDim.x;
         const long long idx = round * n + ((round & 1) ? n - 1 - blockIdx.x : blockIdx.x);
         ++round;
         for (; seq < A.batch.seqs; ++seq) {
             const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
             if (!s.ok && report) atomicOr(A.status, STATUS_INDEX);
-            const int all = s.n * A.group;
-            const int tiles = (all + kPromptRows - 1) / kPromptRows;
-            const long long cnt = (long long)tiles * A.cache.heads;
+            const int all = tiles(A, s);
+            const long long cnt = (long long)all * A.cache.heads;
             if (idx < first + cnt) {
                 const long long local = idx - first;
                 const int up = (int)(local / A.cache.heads);
-                it.s = s;
-                it.seq = seq;
-                it.head = (int)(local - (long long)up * A.cache.heads);
-                it.row0 = (tiles - 1 - up) * kPromptRows;
-                it.steps = 0;
-                for (int t = 0; t < 2; ++t) {
-                    const int r0 = it.row0 + 128 * t;
-                    it.rows[t] = min(max(all - r0, 0), 128);
-                    it.nt[t] = it.rows[t] == 0 ? 0
-                                               : (limit(A, s, r0 + it.rows[t] - 1) + kPromptStep - 1) / kPromptStep;
-                    it.steps = max(it.steps, (it.nt[t] + 1) / 2);
-                }
+                fill(A, s, all - 1 - up, (int)(local - (long long)up * A.cache.heads));
                 return;
             }
             first += cnt;
         }
-        it.seq = -1;
     }
     // positions below it are seen by the row
     __device__ __forceinline__ static int limit(const AttArgs &A, const KvSeq &s, int row) {
@@ -122,6 +166,8 @@ struct __align__(1024) PromptSmem {
     // keys, E and 2^-E of the values
     float kf[8][4], ve[8][4], vi[8][4];
     PromptWalk walk[14];                         // of each warp
+    long long plan_units, plan_items;
+    long long plan[kPromptPlan];                 // position tiles of each sequence
     uint32_t tmem;
     int abort;
 };
@@ -184,9 +230,60 @@ __host__ __device__ constexpr int prompt_order(int p) {
     return CODES == CODES_INT4 ? (p & 1) * 4 + (p >> 1) : p;
 }
 
+// Whether this call's items are cut into equal shares, and where this CTA's
+// share begins.  Whole items take ceil(items / CTAs) rounds of the mean item;
+// shares take the mean load and kPromptJoin tiles for writing and joining the
+// pieces (256 rows of float32 each: about 12 us, measured as two to four
+// position tiles a CTA; items are only cut where that leaves a gain).
+template <class Smem>
+__device__ __forceinline__ void prompt_plan(const AttArgs &A, Smem &sm, int warp, int lane) {
+    const int seqs = A.batch.seqs, heads = A.cache.heads, n = gridDim.x;
+    __syncthreads();                             // (the sums are zero)
+    for (int b = warp; b < seqs; b += kPromptThreads / 32) {
+        const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
+        if (!s.ok && blockIdx.x == 0 && lane == 0) atomicOr(A.status, STATUS_INDEX);
+        const int tiles = PromptWalk::tiles(A, s);
+        long long sum = 0;
+        for (int i = lane; i < tiles; i += 32) sum += max(1, PromptWalk::span(A, s, i));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) {
+            sm.plan[b] = sum * heads;
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sm.plan_units), (unsigned long long)(sum * heads));
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sm.plan_items), (unsigned long long)tiles * heads);
+        }
+    }
+    __syncthreads();
+    const long long units = sm.plan_units, items = sm.plan_items;
+    if (items == 0 || (items + n - 1) / n * units * n <= items * (units + (long long)kPromptJoin * n)) return;
+    // the place of unit u0, by one thread of each warp for its own walk
+    const long long u0 = units * blockIdx.x / n, u1 = units * (blockIdx.x + 1) / n;
+    if (lane == 0) {
+        PromptWalk &w = sm.walk[warp];
+        w.left = u1 - u0;
+        long long at = u0;
+        int b = 0;
+        while (b < seqs && at >= sm.plan[b]) at -= sm.plan[b++];
+        w.seq = b;
+        if (b < seqs && w.left > 0) {
+            const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
+            int tile = PromptWalk::tiles(A, s) - 1;
+            long long len = max(1, PromptWalk::span(A, s, tile));
+            while (at >= len * heads) {
+                at -= len * heads;
+                --tile;
+                len = max(1, PromptWalk::span(A, s, tile));
+            }
+            w.tile = tile;
+            w.head = (int)(at / len);
+            w.t = (int)(at - w.head * len);
+        }
+    }
+}
+
 template <int CODES, int GS, int G, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-attend_prompt_kernel(const AttArgs A) {
+attend_prompt_kernel(const AttArgs A, int split) {
     using Smem = PromptSmem<D>;
     constexpr int SB = D / G * (GS == SC_BF16 ? 2 : 1);
     grid_dependency_begin();
@@ -212,14 +309,28 @@ attend_prompt_kernel(const AttArgs A) {
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (lane == 0) sm.walk[warp].seq = 0, sm.walk[warp].round = 0, sm.walk[warp].first = 0;
+    if (lane == 0) {
+        PromptWalk &w = sm.walk[warp];
+        w.seq = w.round = w.head = w.t = 0;
+        w.tile = -1;
+        w.first = 0;
+        w.left = -1;
+    }
+    if (threadIdx.x == 0) {
+        sm.plan_units = sm.plan_items = 0;
+        AttMeta m;
+        m.units = 0;
+        m.last = m.rows = m.row0 = m.head = m.token0 = m.pad = 0;
+        A.meta[blockIdx.x] = m;
+    }
     const PromptItem &it = sm.walk[warp].it;
     if (warp == 12) tc::tmem_alloc<512>(&sm.tmem);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = sm.tmem;
-    // columns: S (and P over it) of tile 0, of tile 1, O of tile 0, of tile 1
+    if (split) prompt_plan(A, sm, warp, lane);
+    // TMEM columns: S (and P over it) of row tile 0, of row tile 1, O of both
 
     if (warp < 8) {
         // ---------------- softmax: thread = row ----------------
@@ -238,7 +349,8 @@ attend_prompt_kernel(const AttArgs A) {
         };
         while (live && sm.walk[warp].next(A, false)) {
             const int row = it.row0 + 128 * t + row_in;
-            const int nt = it.nt[t];
+            // steps of this piece (none where the row tile sees less than its start)
+            const int nt = max(min(it.nt[t], 2 * it.t1) - 2 * it.t0, 0);
             const bool valid = row_in < it.rows[t];
             const int tok = row / A.group;
             const int64_t qrow = it.s.s0 + tok, qhead = (int64_t)it.head * A.group + row - tok * A.group;
@@ -273,13 +385,18 @@ attend_prompt_kernel(const AttArgs A) {
                 const float fac = A.scale_log2 * pow2f(e - 13);
                 tc::fence_async();
                 tc::bar_arrive(&sm.q_full[t]);
-                int seen = valid ? PromptWalk::limit(A, it.s, row) : 0x7fffffff;   // columns below it count
+                int seen = valid ? PromptWalk::limit(A, it.s, row) - it.t0 * kPromptTile : 0x7fffffff;   // columns below it count
 
                 for (int j = 0; j < nt; ++j, seen -= kPromptStep) {
                     const int half = mine & 1;                          // of the score columns, in turn
                     const uint32_t cols = s_addr + 64 * half;
                     bool ok = tc::bar_wait(&sm.s_full[t][half], (mine >> 1) & 1, abort, A.status);
                     if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+                    if ((warp & 3) * 32 >= it.rows[t]) {                // no row of this warp's: P may be anything
+                        tc::bar_arrive(&sm.p_full[t][half]);
+                        ++mine;
+                        continue;
+                    }
                     tc::fence_after();
                     uint32_t x[2][32];
 #pragma unroll
@@ -364,9 +481,44 @@ attend_prompt_kernel(const AttArgs A) {
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::fence_after();
             }
-            done += it.steps;
+            done += it.t1 - it.t0;
             // ---- the row of the output
-            if (it.rows[t] > 0) {
+            const bool whole = it.t0 == 0 && it.t1 == it.steps;
+            if (!whole) {
+                // a piece: the unnormalized row, its maximum and sum, for the
+                // join; columns of 4 channels by rows, so that a warp's stores
+                // are contiguous
+                const int slot = 2 * (int)blockIdx.x + (it.t0 == 0 ? 1 : 0), prow = 128 * t + row_in;
+                float4 *const dst = reinterpret_cast<float4 *>(A.part) + (int64_t)slot * (D / 4) * kPromptRows + prow;
+                if ((warp & 3) * 32 < it.rows[t]) {
+#pragma unroll 2
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                        if (nt > 0) tc::tmem_load8(o_addr + 8 * c, o);
+                        float y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[prompt_order<CODES>(k)] = __uint_as_float(o[k]) * pow2f(-kPromptK0);
+                        dst[(2 * c) * kPromptRows] = make_float4(y[0], y[1], y[2], y[3]);
+                        dst[(2 * c + 1) * kPromptRows] = make_float4(y[4], y[5], y[6], y[7]);
+                    }
+                    A.part_ml[slot * kPromptRows + prow] = make_float2(m, l);
+                }
+                if (threadIdx.x == 0 && it.t0 == 0) {
+                    // the last share with a piece of this item: the one of its last tile
+                    const long long units = sm.plan_units, n = gridDim.x;
+                    const long long end = units * (blockIdx.x + 1) / n - it.t1 + it.steps;
+                    AttMeta mt;
+                    mt.units = units;
+                    mt.last = (int)min(n - 1, (end * n - 1) / units);
+                    mt.rows = it.rows[0] + it.rows[1];
+                    mt.row0 = it.row0;
+                    mt.head = it.head;
+                    mt.token0 = it.s.s0;
+                    mt.pad = 0;
+                    A.meta[blockIdx.x] = mt;
+                }
+                tc::fence_before();
+            } else if (it.rows[t] > 0) {
                 const float inv = (nt == 0 || m == -INFINITY) ? 0.0f : pow2f(-kPromptK0) / l;
                 uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
 #pragma unroll 2
@@ -394,7 +546,7 @@ attend_prompt_kernel(const AttArgs A) {
         int done = 0;
         bool live = true;
         while (live && sm.walk[warp].next(A, blockIdx.x == 0 && w == 0)) {
-            if (it.steps == 0) continue;
+            if (it.t1 == it.t0) continue;
             const int last = it.row0 + it.rows[0] + it.rows[1] - 1;
             const int hi = PromptWalk::limit(A, it.s, last);
             const auto place = [&](int j) -> int64_t {
@@ -406,13 +558,14 @@ attend_prompt_kernel(const AttArgs A) {
             };
             // loads run ahead: a tile's rows are looked up two tiles before
             // it is expanded, its scales and key codes loaded one before
-            int64_t at = place(0), at_next = place(1);
+            int64_t at = place(it.t0), at_next = place(it.t0 + 1);
             uint4 kc[D / 32], vc[D / 32];
             ScaleWords<SB> ks, vs, vs_next;
             prompt_codes<D>(kc, A.cache.k_codes, at);
             prompt_scales(ks, A.cache.k_scales, at);
             prompt_scales(vs, A.cache.v_scales, at);
-            for (int j = 0; j < it.steps; ++j) {
+            const int t0 = it.t0, tiles = it.t1 - t0;
+            for (int j = 0; j < tiles; ++j) {
                 const int n = done + j, st = n & 1, ph = ((n >> 1) & 1) ^ 1;
                 prompt_codes<D>(vc, A.cache.v_codes, at);
                 // the exponents of both go with the keys: the softmax that
@@ -434,7 +587,7 @@ attend_prompt_kernel(const AttArgs A) {
                 prompt_codes<D>(kc, A.cache.k_codes, at);
                 prompt_scales(ks, A.cache.k_scales, at);
                 prompt_scales(vs_next, A.cache.v_scales, at);
-                at_next = place(j + 2);
+                at_next = place(t0 + j + 2);
                 ok = n < 2 || tc::bar_wait(&sm.v_empty[st], ph, abort, A.status);
                 if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
                 prompt_expand<CODES, GS, G, D, SB>(vc, vs, ev, sm.v[st], row);
@@ -443,7 +596,7 @@ attend_prompt_kernel(const AttArgs A) {
                 if (lane == 0) tc::bar_arrive(&sm.v_full[st]);
                 vs = vs_next;
             }
-            done += it.steps;
+            done += tiles;
         }
     } else {
         // ---------------- MMA issue ----------------
@@ -460,7 +613,7 @@ attend_prompt_kernel(const AttArgs A) {
         const uint64_t v_desc = tc::desc_n_major(tc::smem_addr(sm.v[0]), 16384);
         const uint32_t s_col = tmem + 128 * t, o_col = tmem + 256 + D * t;
         while (live && sm.walk[warp].next(A, false)) {
-            const int steps = it.steps, nt = it.nt[t];
+            const int steps = it.t1 - it.t0, nt = max(min(it.nt[t], 2 * it.t1) - 2 * it.t0, 0);
             // S = Q K^T of step i (64 positions) into its half of the columns
             const auto scores = [&](int i) {
                 const int n = done + (i >> 1);
@@ -529,27 +682,95 @@ attend_prompt_kernel(const AttArgs A) {
     }
 }
 
+// Joins the pieces of the items that were cut: CTA (i, g) takes rows 32 g ..
+// of the one that starts in share i; lane = row, a warp takes a quarter of the
+// channels.
+template <int D>
+__global__ void __launch_bounds__(128)
+attend_prompt_join_kernel(const AttArgs A, int n) {
+    grid_dependency_begin();
+    constexpr int COLS = D / 16;                 // of 4 channels, per warp
+    const AttMeta mt = A.meta[blockIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 32 * blockIdx.y + lane;
+    if ((int)(32 * blockIdx.y) >= mt.rows) return;
+    const bool valid = row < mt.rows;
+    const int i0 = blockIdx.x, last = mt.last;
+    const auto piece = [&](int i) {             // slot, or -1
+        if (mt.units < n && i > i0 && mt.units * i / n >= mt.units * (i + 1) / n) return -1;
+        return 2 * i + (i == i0 ? 1 : 0);
+    };
+    float mx = -INFINITY;
+    for (int i = i0; i <= last; ++i) {
+        const int k = piece(i);
+        if (k >= 0 && valid) mx = max_nan(mx, A.part_ml[k * kPromptRows + row].x);
+    }
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    float4 acc[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) acc[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+    for (int i = i0; i <= last; ++i) {
+        const int k = piece(i);
+        if (k < 0 || !valid) continue;
+        const float2 ml = A.part_ml[k * kPromptRows + row];
+        const float f = ex2(ml.x - base);
+        sum = fmaf(ml.y, f, sum);
+        const float4 *const src = reinterpret_cast<const float4 *>(A.part) +
+                                  ((int64_t)k * (D / 4) + warp * COLS) * kPromptRows + row;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+            const float4 v = src[c * kPromptRows];
+            acc[c].x = fmaf(v.x, f, acc[c].x);
+            acc[c].y = fmaf(v.y, f, acc[c].y);
+            acc[c].z = fmaf(v.z, f, acc[c].z);
+            acc[c].w = fmaf(v.w, f, acc[c].w);
+        }
+    }
+    if (!valid) return;
+    const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+    const int rr = mt.row0 + row, tok = rr / A.group;
+    uint16_t *const dst = A.out + (mt.token0 + tok) * A.out_token +
+                          (int64_t)(mt.head * A.group + rr - tok * A.group) * A.out_head + warp * (D / 4);
+#pragma unroll
+    for (int c = 0; c < COLS; c += 2) {
+        uint32_t h[4];
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[0]) : "f"(acc[c].y * inv), "f"(acc[c].x * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[1]) : "f"(acc[c].w * inv), "f"(acc[c].z * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[2]) : "f"(acc[c + 1].y * inv), "f"(acc[c + 1].x * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[3]) : "f"(acc[c + 1].w * inv), "f"(acc[c + 1].z * inv));
+        *reinterpret_cast<uint4 *>(dst + 4 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+
 template <int CODES, int GS, int G, int D>
 cudaError_t launch_attend_prompt(AttendLaunch &L) {
-    const AttArgs A = att_args(L, kAttRowsMax);
+    const AttArgs A = att_args(L, 2 * kPromptCtas, kPromptRows);
     const auto kern = attend_prompt_kernel<CODES, GS, G, D>;
     constexpr size_t bytes = sizeof(PromptSmem<D>) + 1024;
     static_assert(bytes <= 232448, "shared memory of the prompt kernel");
     static std::atomic<bool> done[64];
     cudaError_t e = smem_opt_in(kern, bytes, done);
     if (e != cudaSuccess) return e;
-    const int64_t rows = L.tokens * A.group;
-    const int64_t items = ((rows + kPromptRows - 1) / kPromptRows + L.batch.seqs) * L.cache.heads;
-    L.launches = 1;
-    return launch_k(kern, dim3((unsigned)std::min<int64_t>(items, 148)), dim3(kPromptThreads), bytes, L.stream, A);
+    // Whether items may be cut at all, by what the host knows (the kernel
+    // decides): at least lo items of at most `longest` tiles, so whole items
+    // lose at most (n - 1) / lo of the time (exactly known for one sequence).
+    const int64_t n = kPromptCtas, lo = (L.tokens * A.group + kPromptRows - 1) / kPromptRows * L.cache.heads;
+    const int64_t longest = ((int64_t)L.batch.max_pages * L.cache.page_size + kPromptTile - 1) / kPromptTile;
+    const int64_t most = (lo + (int64_t)(L.batch.seqs - 1) * L.cache.heads) * std::max<int64_t>(longest, 1);
+    const double loss = L.batch.seqs == 1 ? (double)((lo + n - 1) / n * n) / lo - 1.0 : (double)(n - 1) / lo;
+    const int split = L.batch.seqs <= kPromptPlan && longest > 1 && loss > (double)kPromptJoin * n / most;
+    const int64_t items = lo + (int64_t)L.batch.seqs * L.cache.heads;
+    L.launches = split ? 2 : 1;
+    e = launch_k(kern, dim3((unsigned)(split ? n : std::min<int64_t>(items, n))), dim3(kPromptThreads), bytes, L.stream,
+                 A, split);
+    if (e != cudaSuccess || !split) return e;
+    return launch_k(attend_prompt_join_kernel<D>, dim3((unsigned)n, kPromptRows / 32), dim3(128), 0, L.stream, A, (int)n);
 }
 
 template <int CODES, int GS, int G, int D>
 cudaError_t launch_attend_d(AttendLaunch &L) {
-    const int64_t rows = L.tokens * (L.q_heads / L.cache.heads);
-    if (rows > 48 * (int64_t)L.batch.seqs) return launch_attend_prompt<CODES, GS, G, D>(L);
-    if (rows <= 8 * (int64_t)L.batch.seqs) return launch_attend_split<CODES, GS, G, D, 1>(L);
-    return launch_attend_split<CODES, GS, G, D, 2>(L);
+    if (attend_by_prompt(L.tokens, L.q_heads, L.cache.heads, L.batch.seqs)) return launch_attend_prompt<CODES, GS, G, D>(L);
+    return launch_attend_split<CODES, GS, G, D, 1>(L);
 }
 
 template <int CODES, int GS>
