@@ -270,10 +270,6 @@ struct ScaleWords {
             else return v == 0 ? -200 : max((int)((v & 0x7Fu) >> 3), 1) - 7;
         }
     }
-    __device__ __forceinline__ static void zero(uint8_t *p) {
-#pragma unroll
-        for (int i = 0; i < SB; ++i) p[i] = 0;
-    }
 };
 
 template <int CODES, int GS, int G, int D, int NB>
@@ -808,7 +804,7 @@ attend_split_kernel(const AttArgs A) {
                 acc.w = fmaf(v.w, f, acc.w);
             }
             if (whole) {
-                const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 const int rr = row0 + row, tok = rr / A.group;
                 uint2 v;
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(acc.y * inv), "f"(acc.x * inv));
@@ -894,7 +890,7 @@ attend_join_kernel(const AttArgs A, int n) {
         acc.w += v.w;
         sum += s_sum[w];
     }
-    const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int rr = mt.row0 + row, tok = rr / A.group;
     uint2 v;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(acc.y * inv), "f"(acc.x * inv));

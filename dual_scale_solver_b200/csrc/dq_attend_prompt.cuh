@@ -519,7 +519,7 @@ attend_prompt_kernel(const AttArgs A, int split) {
                 }
                 tc::fence_before();
             } else if (it.rows[t] > 0) {
-                const float inv = (nt == 0 || m == -INFINITY) ? 0.0f : pow2f(-kPromptK0) / l;
+                const float inv = l == 0.0f ? 0.0f : pow2f(-kPromptK0) / l;      // (l is NaN where Q is)
                 uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
 #pragma unroll 2
                 for (int c = 0; c < D / 8; ++c) {
@@ -727,7 +727,7 @@ attend_prompt_join_kernel(const AttArgs A, int n) {
         }
     }
     if (!valid) return;
-    const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int rr = mt.row0 + row, tok = rr / A.group;
     uint16_t *const dst = A.out + (mt.token0 + tok) * A.out_token +
                           (int64_t)(mt.head * A.group + rr - tok * A.group) * A.out_head + warp * (D / 4);

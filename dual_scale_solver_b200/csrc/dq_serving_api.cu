@@ -29,7 +29,8 @@ dq_status check_cache(const dq_kv_cache *c, const dq_kv_batch *b, const dq_forma
     if (c->page_size <= 0 || c->page_size % 16 || c->heads <= 0 || c->pages < 0) return DQ_ERR_SHAPE;
     if (c->heads > 65535 || c->pages > INT32_MAX) return DQ_ERR_SHAPE;
     if (b->seqs < 0 || b->max_pages < 0 || b->table_stride < b->max_pages) return DQ_ERR_SHAPE;
-    if ((int64_t)b->max_pages * c->page_size > INT32_MAX) return DQ_ERR_SHAPE;
+    // (the kernels look up to 4095 positions past a sequence's end in 32 bits)
+    if ((int64_t)b->max_pages * c->page_size > INT32_MAX - 4095) return DQ_ERR_SHAPE;
     if (tokens < 0 || tokens > INT32_MAX) return DQ_ERR_SHAPE;
     if (tokens == 0 || b->seqs == 0) return DQ_OK;
     if (!b->starts || !b->kv_lens) return DQ_ERR_ARG;

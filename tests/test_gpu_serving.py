@@ -280,6 +280,142 @@ def test_attention_prompts(name, G, dim, seqs):
         _check_attention(B, q, cache, values, causal=causal)
 
 
+@pytest.mark.parametrize("name,G", [("int4_bf16", 64), ("mxint4", 32), ("mxfp4", 32), ("nvfp4_ts1", 16)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("seqs,group", [([(40, 6000)], 4), ([(300, 2500), (0, 700), (3, 0), (70, 50)], 2)])
+def test_attention_prompts_cut_and_joined(name, G, dim, seqs, group):
+    """Few row tiles over many positions: shares of the grid begin and end
+    inside them.  Row tiles that do not fill the 256 rows, rows that see
+    nothing, more CTAs than positions; the same bits again."""
+    B = Batch(seqs, 16, 1, dim, name, G, pad=2)
+    cache, values = B.fill()
+    q = bf16_from(B.rng, (B.tokens, group, dim)).cuda()
+    out = torch.full_like(q, 5.0)
+    for causal in (True, False):
+        a = _check_attention(B, q, cache, values, causal=causal, out=out).clone()
+        assert bool((a[int(B.starts[-1]):] == 5.0).all())
+        b = dq.kv_attention(q, cache, *B.device(), B.fmt, causal=causal)
+        n = int(B.starts[-1])
+        assert torch.equal(a[:n], b[:n])
+
+
+def test_attention_prompts_many_sequences():
+    """More row tiles than CTAs, sequences of every length; and more sequences
+    than shares are planned for."""
+    rng = np.random.default_rng(11)
+    for count, longest in ((200, 60), (1100, 12)):
+        seqs = [(int(n), int(n + m)) for n, m in zip(rng.integers(0, longest, count), rng.integers(0, 50, count))]
+        seqs[count // 2] = (longest, 900)
+        B = Batch(seqs, 16, 2, 64, "mxfp4", 32)
+        cache, values = B.fill()
+        q = bf16_from(B.rng, (B.tokens, 8, 64)).cuda()
+        _check_attention(B, q, cache, values)
+
+
+@pytest.mark.parametrize("name,G", [("int4_bf16", 64), ("nvfp4_ts1", 16)])
+@pytest.mark.parametrize("seqs", [[(1, 300), (1, 2000)], [(20, 300), (30, 2000)]])
+def test_attention_nonfinite_queries_stay_in_their_rows(name, G, seqs):
+    B = Batch(seqs, 16, 2, 64, name, G)
+    cache, values = B.fill()
+    q = bf16_from(B.rng, (B.tokens, 8, 64)).cuda()
+    want = _check_attention(B, q, cache, values)
+    bad = q.clone()
+    bad[0, 1, 5], bad[B.tokens - 1, 6, 63] = float("nan"), float("nan")
+    got = dq.kv_attention(bad, cache, *B.device(), B.fmt)
+    assert bool(got[0, 1].isnan().all()) and bool(got[B.tokens - 1, 6].isnan().all())
+    got[0, 1], got[B.tokens - 1, 6] = want[0, 1], want[B.tokens - 1, 6]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_bad_places_are_flagged_and_touch_nothing_else(new):
+    """Pages out of range, lengths beyond the table, starts that decrease or
+    pass the last row: flagged, and the other sequences' results are those of
+    the clean batch."""
+    B = Batch([(new, 200)] * 4, 16, 2, 64, "mxfp4", 32, spare=0)
+    cache, values = B.fill()
+    q = bf16_from(B.rng, (B.tokens, 8, 64)).cuda()
+    k, v = (bf16_from(B.rng, (B.tokens, 2, 64)).cuda() for _ in range(2))
+    starts, lens, table = B.device()
+    want = _check_attention(B, q, cache, values)
+    whole = [t.clone() for t in cache]
+    dq.kv_append(k, v, cache, starts, lens, table, B.fmt)
+    after = [t.clone() for t in cache]
+    kk, vv = dq.kv_read(cache, starts, lens, table, B.fmt, B.tokens)
+    assert dq.last_device_status() == 0
+    last = table[2, 12].item()
+
+    def put(t, at, value):
+        t = t.clone()
+        t[at] = value
+        return t
+
+    bad = [(starts, lens, put(table, (2, 12), x)) for x in (-1, B.pages, 1 << 30)]
+    bad += [(starts, put(lens, 2, x), table) for x in (-1, 16 * table.shape[1] + 1, 0x7FFFFFFF)]
+    rows = slice(2 * new, 3 * new)
+    for meta in bad:
+        for t, w in zip(cache, whole):
+            t.copy_(w)
+        out = torch.full_like(q, 5.0)
+        dq.kv_attention(q, cache, *meta, B.fmt, out=out)
+        assert dq.last_device_status() == -12
+        out[rows] = want[rows]
+        assert torch.equal(out, want)
+        dq.kv_append(k, v, cache, *meta, B.fmt)
+        assert dq.last_device_status() == -12
+        for t, w, a in zip(cache, whole, after):
+            same = torch.arange(B.pages, device="cuda") != last           # (its new tokens' last page)
+            assert torch.equal(t[last], w[last])
+            if meta[1] is lens and new == 1:
+                assert torch.equal(t[same], a[same])
+        for t, a in zip(cache, after):
+            t.copy_(a)
+        k2, v2 = dq.kv_read(cache, *meta, B.fmt, B.tokens)
+        assert dq.last_device_status() == -12
+        for x, y in ((k2, kk), (v2, vv)):
+            x[rows] = y[rows]
+            assert torch.equal(x, y)
+    for t, w in zip(cache, whole):
+        t.copy_(w)
+    # starts: sequence 1 beyond the rows or behind its own start: 0 is still answered
+    for x in (B.tokens + 1, -1):
+        out = dq.kv_attention(q, cache, put(starts, 2, x), lens, table, B.fmt)
+        assert dq.last_device_status() == -12
+        assert torch.equal(out[:new], want[:new])
+        dq.kv_append(k, v, cache, put(starts, 2, x), lens, table, B.fmt)
+        assert dq.last_device_status() == -12
+        for t, w in zip(cache, whole):
+            t.copy_(w)
+
+
+def test_places_past_32_bits():
+    """Pages whose codes lie more than 2^32 bytes into the cache, the same
+    bits as in a small one."""
+    B = Batch([(1, 700), (2, 90)], 64, 8, 128, "mxfp4", 32)
+    P = Batch([(60, 700), (30, 90)], 64, 8, 128, "mxfp4", 32)
+    for b in (B, P):
+        small, _ = b.fill()
+        shift = (1 << 32) // (8 * 64 * 64) + 7
+        big = tuple(torch.empty((b.pages + shift,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in small)
+        for t, s in zip(big, small):
+            t[shift:] = s
+        starts, lens, table = b.device()
+        far = torch.where(table < b.pages, table + shift, table)
+        q = bf16_from(b.rng, (b.tokens, 16 if b is P else 8, 128)).cuda()
+        k, v = (bf16_from(b.rng, (b.tokens, 8, 128)).cuda() for _ in range(2))
+        got = []
+        for cache, tab in ((small, table), (big, far)):
+            dq.kv_append(k, v, cache, starts, lens, tab, b.fmt)
+            got.append((dq.kv_attention(q, cache, starts, lens, tab, b.fmt),
+                        *dq.kv_read(cache, starts, lens, tab, b.fmt, b.tokens)))
+        assert dq.last_device_status() == 0
+        for x, y in zip(*got):
+            assert torch.equal(x, y)
+        for t, s in zip(big, small):
+            assert torch.equal(t[shift:], s)
+        del big
+
+
 def test_attention_strides_scale_and_repeatability():
     B = Batch([(1, 500), (3, 77), (1, 2000)], 32, 2, 128, "mxfp4", 32)
     cache, values = B.fill()
@@ -407,6 +543,29 @@ def test_explicit_stream():
     a = dq.kv_attention(q, cache, *B.device(), B.fmt, stream=side)
     side.synchronize()
     assert torch.equal(a, want)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace."""
+    B = Batch([(1, 3000), (1, 700)], 16, 2, 64, "mxfp4", 32)
+    P = Batch([(90, 1500)], 16, 2, 64, "mxfp4", 32)
+    work = []
+    for b in (B, P):
+        cache, values = b.fill()
+        q = bf16_from(b.rng, (b.tokens, 8, 64)).cuda()
+        work.append((b, cache, q, b.device(), _check_attention(b, q, cache, values)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = []
+    for i in range(20):
+        for j, s in enumerate(streams):
+            b, cache, q, meta, want = work[(i + j) % 2]
+            with torch.cuda.stream(s):
+                outs.append((dq.kv_attention(q, cache, *meta, b.fmt), want))
+    torch.cuda.synchronize()
+    for got, want in outs:
+        assert torch.equal(got, want)
+    assert dq.last_device_status() == 0
 
 
 def test_a_layer_with_quantized_products():

@@ -89,6 +89,7 @@ BAD_PLACES = [
     (dict(batch=_batch(kv_lens=None)), -1), (dict(batch=_batch(block_table=None)), -1),
     (dict(batch=_batch(starts=4098)), -9),
     (dict(batch=_batch(max_pages=1 << 28, table_stride=1 << 28)), -2),   # positions past 32 bits
+    (dict(batch=_batch(max_pages=(1 << 27) - 255, table_stride=1 << 28)), -2),
 ]
 
 
@@ -131,6 +132,8 @@ def test_attention_refusals():
     assert _attend(tokens=1 << 30, q_heads=128, ot=1 << 14) == -2  # rows past 32 bits
     for kw, status in BAD_PLACES:
         assert _attend(**kw) == status, kw
+    most = _batch(max_pages=(1 << 27) - 256, table_stride=1 << 28)  # 2^31 - 4096 positions
+    assert _attend(batch=most, ws=None) == -7
 
 
 def test_attention_workspace():
