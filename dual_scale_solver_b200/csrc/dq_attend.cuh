@@ -44,10 +44,23 @@ constexpr int kAttTile = 32;                       // tokens per warp step
 constexpr int kAttUnit = kAttTile * kAttWarps;     // tokens per unit
 constexpr int kAttCtas = 2 * 148;
 
-// Calls of more than 8 query rows (new tokens x heads of a group) per sequence
-// go to the tcgen05 kernel, which takes 256 rows at a time.
-inline bool attend_by_prompt(int64_t tokens, int32_t q_heads, int32_t heads, int32_t seqs) {
-    return tokens * (q_heads / heads) > 8 * (int64_t)seqs;
+// Sequences of up to 32 query rows (new tokens x heads of a group) are this
+// file's, longer ones the tcgen05 kernel's, which takes 256 rows at a time.
+// 8 sequences of 8 cache heads, D = 128: 32 rows each over 4001 positions 31
+// us (MXFP4) and 37 (NVFP4) here against 40 there, over 16000 87 and 112
+// against 91 and 97; 16 rows 22 to 69 us against 39 to 96.
+constexpr int kAttFew = 32;
+enum { ATT_FEW = 1, ATT_MANY = 2 };
+
+// The kernels of a call; which of two takes a sequence is decided on the
+// device, where its length is known.  Calls of a token per sequence in the mean
+// (or fewer) are single tokens: the other kernel's launch, about 2 us of a
+// call that may take 10, is saved.
+inline int attend_kernels(int64_t tokens, int32_t q_heads, int32_t heads, int32_t seqs) {
+    const int64_t group = q_heads / heads;
+    if (tokens * group <= kAttFew) return ATT_FEW;
+    if (seqs == 1 || group > kAttFew) return ATT_MANY;
+    return tokens <= seqs ? ATT_FEW : ATT_FEW | ATT_MANY;
 }
 
 // What CTA i leaves for the joining kernel: the segment that starts (and
@@ -69,6 +82,7 @@ struct AttArgs {
     int64_t out_token, out_head;
     int64_t tokens;
     int group;              // query heads per cache head
+    int few;                // sequences of up to so many rows are dq_attend.cuh's
     float scale_log2;       // scale * log2(e)
     uint32_t k16;           // 16
     int causal;
@@ -87,11 +101,12 @@ struct AttSpan {            // a sequence's segments and units
 };
 
 template <int ROWS>
-__device__ __forceinline__ AttSpan att_span(const KvSeq &s, int group, int heads) {
+__device__ __forceinline__ AttSpan att_span(const AttArgs &A, const KvSeq &s) {
     AttSpan a;
-    a.qt = (int)(((long long)s.n * group + ROWS - 1) / ROWS);
+    const long long rows = (long long)s.n * A.group;
+    a.qt = rows > A.few ? 0 : (int)((rows + ROWS - 1) / ROWS);
     a.kvt = max(1, (s.len + kAttUnit - 1) / kAttUnit);
-    a.units = (long long)a.qt * heads * a.kvt;
+    a.units = (long long)a.qt * A.cache.heads * a.kvt;
     return a;
 }
 
@@ -324,7 +339,7 @@ attend_split_kernel(const AttArgs A) {
     for (int b = tid; b < seqs; b += kAttThreads) {
         const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
         if (!s.ok && me == 0) atomicOr(A.status, STATUS_INDEX);
-        mine = att_span<ROWS>(s, A.group, heads).units;
+        mine = att_span<ROWS>(A, s).units;
         total += mine;
     }
     const auto block_scan = [&](long long v, long long &all) {     // inclusive
@@ -364,7 +379,7 @@ attend_split_kernel(const AttArgs A) {
         for (int b0 = 0; b0 < seqs; b0 += kAttThreads) {
             const int b = b0 + tid;
             long long v = 0, all;
-            if (b < seqs) v = att_span<ROWS>(kv_seq(A.batch, A.cache.page_size, A.tokens, b), A.group, heads).units;
+            if (b < seqs) v = att_span<ROWS>(A, kv_seq(A.batch, A.cache.page_size, A.tokens, b)).units;
             const long long in = base + block_scan(v, all);
             if (v > 0 && in - v <= u0 && u0 < in) {
                 s_seq = b;
@@ -388,7 +403,7 @@ attend_split_kernel(const AttArgs A) {
 
     for (long long u = u0; u < u1;) {
         const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
-        const AttSpan sp = att_span<ROWS>(s, A.group, heads);
+        const AttSpan sp = att_span<ROWS>(A, s);
         if (u >= first + sp.units) {
             first += sp.units;
             ++seq;
@@ -901,7 +916,7 @@ attend_join_kernel(const AttArgs A, int n) {
 
 // ---- launch
 
-inline AttArgs att_args(const AttendLaunch &L, int slots, int rows) {
+inline AttArgs att_args(const AttendLaunch &L, int slots, int rows, int few) {
     AttArgs A;
     A.q = static_cast<const uint16_t *>(L.q);
     A.q_token = L.q_token;
@@ -912,6 +927,7 @@ inline AttArgs att_args(const AttendLaunch &L, int slots, int rows) {
     A.tokens = L.tokens;
     A.group = L.q_heads / L.cache.heads;
     A.scale_log2 = L.scale * 1.44269504088896341f;
+    A.few = few;
     A.causal = L.causal;
     A.k16 = 16;
     A.cache = L.cache;
@@ -927,19 +943,19 @@ inline AttArgs att_args(const AttendLaunch &L, int slots, int rows) {
 }
 
 template <int CODES, int GS, int G, int D, int NB>
-cudaError_t launch_attend_split(AttendLaunch &L) {
+cudaError_t launch_attend_split(AttendLaunch &L, int few) {
     using Sh = AttShape<CODES, GS, G, D, NB>;
-    const AttArgs A = att_args(L, 2 * kAttCtas, Sh::ROWS);
+    const AttArgs A = att_args(L, 2 * kAttCtas, Sh::ROWS, few);
     const auto kern = attend_split_kernel<CODES, GS, G, D, NB>;
     static std::atomic<bool> done[64];
     cudaError_t e = smem_opt_in(kern, Sh::BYTES, done);
     if (e != cudaSuccess) return e;
     e = launch_k(kern, dim3(kAttCtas), dim3(kAttThreads), Sh::BYTES, L.stream, A);
     if (e != cudaSuccess) return e;
-    L.launches = 1;
+    L.launches += 1;
     // (sequences of at most one unit are never cut)
     if ((int64_t)L.batch.max_pages * L.cache.page_size <= kAttUnit) return cudaSuccess;
-    L.launches = 2;
+    L.launches += 1;
     return launch_k(attend_join_kernel<D, NB>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
 }
 

@@ -5,7 +5,8 @@ namespace dq {
 size_t attend_workspace(int64_t tokens, int32_t q_heads, int32_t heads, int32_t head_dim, int32_t seqs) {
     // two pieces per CTA: rows of float32 sums with their (maximum, sum)
     const size_t row = head_dim * sizeof(float) + sizeof(float2);
-    return attend_by_prompt(tokens, q_heads, heads, seqs)
+    // (calls of both kernels use it one after the other)
+    return attend_kernels(tokens, q_heads, heads, seqs) & ATT_MANY
                ? 2 * kPromptCtas * kPromptRows * row + kPromptCtas * sizeof(AttMeta)
                : 2 * kAttCtas * 8 * row + kAttCtas * sizeof(AttMeta);
 }

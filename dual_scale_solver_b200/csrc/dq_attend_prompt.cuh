@@ -75,12 +75,50 @@ struct PromptWalk {
     // worked out by one lane: registers are short elsewhere).
     __device__ __forceinline__ bool next(const AttArgs &A, bool report) {
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) step(A, report);
+        skip(A, report);
+        if ((threadIdx.x & 31) == 0) step(A);
         __syncwarp();
         return it.seq >= 0;
     }
+    // row tile pairs of a sequence (none of one that the other kernel takes)
     __device__ __forceinline__ static int tiles(const AttArgs &A, const KvSeq &s) {
-        return (int)(((long long)s.n * A.group + kPromptRows - 1) / kPromptRows);
+        const long long rows = (long long)s.n * A.group;
+        return rows <= A.few ? 0 : (int)((rows + kPromptRows - 1) / kPromptRows);
+    }
+    // The place of the next whole item.
+    __device__ __forceinline__ long long index() const {
+        const long long n = gridDim.x;
+        return round * n + ((round & 1) ? n - 1 - blockIdx.x : blockIdx.x);
+    }
+    // Passes over the sequences that have no part in the next piece, 32 at a
+    // time (the whole warp).
+    __device__ __forceinline__ void skip(const AttArgs &A, bool report) {
+        const int lane = threadIdx.x & 31, seqs = A.batch.seqs;
+        const bool cut = left >= 0, stay = cut && tile >= 0;
+        const long long idx = index();
+        int at = seq;
+        long long before = first;
+        __syncwarp();
+        while (!stay && at < seqs) {
+            long long cnt = 0;
+            if (at + lane < seqs) {
+                const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, at + lane);
+                if (!s.ok && report) atomicOr(A.status, STATUS_INDEX);
+                cnt = (long long)tiles(A, s) * A.cache.heads;
+            }
+            long long incl = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, cut ? cnt > 0 : idx < before + incl);
+            const int k = hit ? __ffs(hit) - 1 : 31;
+            before += __shfl_sync(0xffffffffu, hit ? incl - cnt : incl, k);
+            at += hit ? k : 32;
+            if (hit) break;
+        }
+        if (lane == 0) seq = at, first = before;
     }
     // position tiles that row tile pair `tile` sees
     __device__ __forceinline__ static int span(const AttArgs &A, const KvSeq &s, int tile) {
@@ -103,48 +141,30 @@ struct PromptWalk {
         it.t0 = 0;
         it.t1 = it.steps;
     }
-    __device__ __forceinline__ void step(const AttArgs &A, bool report) {
+    __device__ __forceinline__ void step(const AttArgs &A) {
+        const long long local = index() - first;
+        ++round;
         it.seq = -1;
-        if (left >= 0) {
-            while (left > 0 && seq < A.batch.seqs) {
-                const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
-                if (tile < 0) tile = tiles(A, s) - 1;          // a new sequence
-                if (tile < 0) {
-                    ++seq;
-                    continue;
-                }
-                fill(A, s, tile, head);
-                const int take = (int)min(left, (long long)max(it.steps, 1) - t);
-                it.t0 = t;
-                it.t1 = min(t + take, it.steps);
-                left -= take;
-                t += take;
-                if (t >= it.steps) {
-                    t = 0;
-                    if (++head == A.cache.heads) {
-                        head = 0;
-                        if (--tile < 0) ++seq;
-                    }
-                }
-                return;
-            }
+        if (seq >= A.batch.seqs || left == 0) return;
+        const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
+        if (left < 0) {
+            const int up = (int)(local / A.cache.heads);
+            fill(A, s, tiles(A, s) - 1 - up, (int)(local - (long long)up * A.cache.heads));
             return;
         }
-        const long long n = gridDim.x;
-        const long long idx = round * n + ((round & 1) ? n - 1 - blockIdx.x : blockIdx.x);
-        ++round;
-        for (; seq < A.batch.seqs; ++seq) {
-            const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
-            if (!s.ok && report) atomicOr(A.status, STATUS_INDEX);
-            const int all = tiles(A, s);
-            const long long cnt = (long long)all * A.cache.heads;
-            if (idx < first + cnt) {
-                const long long local = idx - first;
-                const int up = (int)(local / A.cache.heads);
-                fill(A, s, all - 1 - up, (int)(local - (long long)up * A.cache.heads));
-                return;
+        if (tile < 0) tile = tiles(A, s) - 1;              // a new sequence
+        fill(A, s, tile, head);
+        const int take = (int)min(left, (long long)max(it.steps, 1) - t);
+        it.t0 = t;
+        it.t1 = min(t + take, it.steps);
+        left -= take;
+        t += take;
+        if (t >= it.steps) {
+            t = 0;
+            if (++head == A.cache.heads) {
+                head = 0;
+                if (--tile < 0) ++seq;
             }
-            first += cnt;
         }
     }
     // positions below it are seen by the row
@@ -293,6 +313,19 @@ attend_prompt_kernel(const AttArgs A, int split) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort = &sm.abort;
     if (threadIdx.x == 0) {
+        AttMeta m;
+        m.units = 0;
+        m.last = m.rows = m.row0 = m.head = m.token0 = m.pad = 0;
+        A.meta[blockIdx.x] = m;
+    }
+    if (A.few) {
+        // nothing to do where every sequence has few rows
+        bool any = false;
+        for (int b = threadIdx.x; b < A.batch.seqs; b += kPromptThreads)
+            any |= PromptWalk::tiles(A, kv_seq(A.batch, A.cache.page_size, A.tokens, b)) > 0;
+        if (!__syncthreads_or(any)) return;
+    }
+    if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(&sm.q_full[i], 128);
             for (int b = 0; b < 2; ++b) {
@@ -318,10 +351,6 @@ attend_prompt_kernel(const AttArgs A, int split) {
     }
     if (threadIdx.x == 0) {
         sm.plan_units = sm.plan_items = 0;
-        AttMeta m;
-        m.units = 0;
-        m.last = m.rows = m.row0 = m.head = m.token0 = m.pad = 0;
-        A.meta[blockIdx.x] = m;
     }
     const PromptItem &it = sm.walk[warp].it;
     if (warp == 12) tc::tmem_alloc<512>(&sm.tmem);
@@ -743,8 +772,8 @@ attend_prompt_join_kernel(const AttArgs A, int n) {
 }
 
 template <int CODES, int GS, int G, int D>
-cudaError_t launch_attend_prompt(AttendLaunch &L) {
-    const AttArgs A = att_args(L, 2 * kPromptCtas, kPromptRows);
+cudaError_t launch_attend_prompt(AttendLaunch &L, int few) {
+    const AttArgs A = att_args(L, 2 * kPromptCtas, kPromptRows, few);
     const auto kern = attend_prompt_kernel<CODES, GS, G, D>;
     constexpr size_t bytes = sizeof(PromptSmem<D>) + 1024;
     static_assert(bytes <= 232448, "shared memory of the prompt kernel");
@@ -754,23 +783,25 @@ cudaError_t launch_attend_prompt(AttendLaunch &L) {
     // Whether items may be cut at all, by what the host knows (the kernel
     // decides): at least lo items of at most `longest` tiles, so whole items
     // lose at most (n - 1) / lo of the time (exactly known for one sequence).
-    const int64_t n = kPromptCtas, lo = (L.tokens * A.group + kPromptRows - 1) / kPromptRows * L.cache.heads;
+    const int64_t n = kPromptCtas, heads = L.cache.heads, seqs = L.batch.seqs, rows = L.tokens * A.group;
+    const int64_t lo = std::max<int64_t>((rows - few * seqs + kPromptRows - 1) / kPromptRows, 0) * heads;
+    const int64_t hi = ((rows + kPromptRows - 1) / kPromptRows + seqs - 1) * heads;
     const int64_t longest = ((int64_t)L.batch.max_pages * L.cache.page_size + kPromptTile - 1) / kPromptTile;
-    const int64_t most = (lo + (int64_t)(L.batch.seqs - 1) * L.cache.heads) * std::max<int64_t>(longest, 1);
-    const double loss = L.batch.seqs == 1 ? (double)((lo + n - 1) / n * n) / lo - 1.0 : (double)(n - 1) / lo;
-    const int split = L.batch.seqs <= kPromptPlan && longest > 1 && loss > (double)kPromptJoin * n / most;
-    const int64_t items = lo + (int64_t)L.batch.seqs * L.cache.heads;
-    L.launches = split ? 2 : 1;
-    e = launch_k(kern, dim3((unsigned)(split ? n : std::min<int64_t>(items, n))), dim3(kPromptThreads), bytes, L.stream,
-                 A, split);
+    const double loss = lo == 0 ? 0.0 : seqs == 1 ? (double)((lo + n - 1) / n * n) / lo - 1.0 : (double)(n - 1) / lo;
+    const int split = seqs <= kPromptPlan && longest > 1 && loss > (double)kPromptJoin * n / (hi * longest);
+    L.launches += split ? 2 : 1;
+    e = launch_k(kern, dim3((unsigned)(split ? n : std::min(hi, n))), dim3(kPromptThreads), bytes, L.stream, A, split);
     if (e != cudaSuccess || !split) return e;
     return launch_k(attend_prompt_join_kernel<D>, dim3((unsigned)n, kPromptRows / 32), dim3(128), 0, L.stream, A, (int)n);
 }
 
 template <int CODES, int GS, int G, int D>
 cudaError_t launch_attend_d(AttendLaunch &L) {
-    if (attend_by_prompt(L.tokens, L.q_heads, L.cache.heads, L.batch.seqs)) return launch_attend_prompt<CODES, GS, G, D>(L);
-    return launch_attend_split<CODES, GS, G, D, 1>(L);
+    const int by = attend_kernels(L.tokens, L.q_heads, L.cache.heads, L.batch.seqs);
+    cudaError_t e = cudaSuccess;
+    if (by & ATT_MANY) e = launch_attend_prompt<CODES, GS, G, D>(L, by & ATT_FEW ? kAttFew : 0);
+    if (e != cudaSuccess || !(by & ATT_FEW)) return e;
+    return launch_attend_split<CODES, GS, G, D, 1>(L, by & ATT_MANY ? kAttFew : INT32_MAX);
 }
 
 template <int CODES, int GS>
