@@ -3,7 +3,7 @@
 //   out = softmax(scale q . k_hat) v_hat,  k_hat = c_k s_k,  v_hat = c_v s_v
 //
 // For single tokens (and drafts of a few) the work is the streaming of codes:
-// each code byte is used for at most 8 NB query rows.  Tensor-core products
+// each code byte is used for at most 8 query rows.  Tensor-core products
 // keep the arithmetic per code low enough to stay near the memory's pace:
 //
 //  S^T = K Q^T   A = 16 tokens x 16 channels of codes as fp16 (exact), B = 8
@@ -14,16 +14,17 @@
 //  O^T = V^T P^T A = 16 channels x 16 tokens of codes as fp16, B = the
 //                probabilities times the tokens' group scales, fp16 both and
 //                their product.  With 2^E the largest value scale of a tile,
-//                scales enter as s 2^(7 - E), probabilities as p 2^(E + 7)
-//                against a running maximum that holds E, so the products
-//                stay below 2^15 and what lies 2^-29 below the largest is
-//                lost; roundings 2^-12 each, below the output type's 2^-9.
+//                scales enter as s 2^(6 - E) (below 2^7), probabilities as p
+//                2^(E + 7 .. 9) against a running maximum that holds E, so
+//                the products stay below 2^16 - 2^8 and what lies 2^-28 below
+//                the largest is lost; roundings 2^-12 each, below the output
+//                type's 2^-9.
 //
 // A query row is one (token, head of the group) pair, so the g heads of a
 // group share every code.  The probabilities pass from the layout of the
 // first product's result to the second's operand with movmatrix.
 //
-// Work: (sequence, cache head, tile of 8 NB rows) segments of 256-token
+// Work: (sequence, cache head, tile of 8 rows) segments of 256-token
 // units, numbered through the batch; CTA i of n takes units [U i / n, U (i+1)
 // / n) (found by a scan over the sequences' lengths on the device, so lengths
 // may differ freely and the call needs no host copy of them).  A segment that
@@ -287,9 +288,9 @@ struct ScaleWords {
     }
 };
 
-template <int CODES, int GS, int G, int D, int NB>
+template <int CODES, int GS, int G, int D>
 struct AttShape {
-    static constexpr int ROWS = 8 * NB;
+    static constexpr int ROWS = 8;
     static constexpr int NG = D / G;
     static constexpr int SB = NG * (GS == SC_BF16 ? 2 : 1);      // scale bytes of a token
     static constexpr int CB = kAttTile * D / 2;                  // code bytes of a warp tile
@@ -297,7 +298,7 @@ struct AttShape {
     static constexpr int STAGE = 2 * CB + 2 * TB;
     // a warp tile's scales by group and token: values' as fp16, keys' as float32
     static constexpr int VS_BYTES = NG * kAttTile * 6;
-    static constexpr int RING_MAX = (112 * 1024 / kAttWarps - VS_BYTES - 64 * NB) / STAGE;
+    static constexpr int RING_MAX = (112 * 1024 / kAttWarps - VS_BYTES - 64) / STAGE;
     static constexpr int RING = RING_MAX > 5 ? 5 : RING_MAX;
     static constexpr int RING_BYTES = kAttWarps * RING * STAGE;
     static constexpr int OST = D + 4;                            // row stride of the joining buffer
@@ -316,10 +317,10 @@ __device__ __forceinline__ uint32_t code_off(int t, int ch) {
     else return (uint32_t)(t * 32 + ((ch ^ ((t >> 2) & 1)) << 4));
 }
 
-template <int CODES, int GS, int G, int D, int NB>
-__global__ void __launch_bounds__(kAttThreads, NB == 1 ? 2 : 1)
+template <int CODES, int GS, int G, int D>
+__global__ void __launch_bounds__(kAttThreads, 2)
 attend_split_kernel(const AttArgs A) {
-    using Sh = AttShape<CODES, GS, G, D, NB>;
+    using Sh = AttShape<CODES, GS, G, D>;
     using Sw = ScaleWords<Sh::SB>;
     constexpr int ROWS = Sh::ROWS, RING = Sh::RING, NJ = D / 32;
     grid_dependency_begin();
@@ -480,16 +481,13 @@ attend_split_kernel(const AttArgs A) {
             cp_commit();
         };
         // (every load that depends on nothing else first)
-        uint4 raw[NB][NJ];
+        uint4 raw[NJ];
+        const int row = row0 + r, tok = row / A.group;
+        const uint16_t *p = A.q + (s.s0 + tok) * A.q_token +
+                            (int64_t)(head * A.group + row - tok * A.group) * A.q_head + 8 * c;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int row = row0 + 8 * nb + r, tok = row / A.group;
-            const uint16_t *p = A.q + (s.s0 + tok) * A.q_token +
-                                (int64_t)(head * A.group + row - tok * A.group) * A.q_head + 8 * c;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                raw[nb][j] = 8 * nb + r < rows ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * j)) : make_uint4(0, 0, 0, 0);
-        }
+        for (int j = 0; j < NJ; ++j)
+            raw[j] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * j)) : make_uint4(0, 0, 0, 0);
         int64_t first_rows[RING];
 #pragma unroll
         for (int i = 0; i < RING; ++i) first_rows[i] = next_row();
@@ -499,58 +497,53 @@ attend_split_kernel(const AttArgs A) {
 
         // ---- the query rows: B operands, and the factor that takes a
         // product of scaled operands to log2 units
-        uint32_t qf[NB][NJ][4];
-        float fac[NB][2];
-        int lim[NB][2];
+        uint32_t qf[NJ][4];
+        float fac[2];
+        int lim[2];
+        uint32_t top = 0;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            uint32_t top = 0;
+        for (int j = 0; j < NJ; ++j) {
+            const uint32_t v[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const uint32_t v[4] = {raw[nb][j].x, raw[nb][j].y, raw[nb][j].z, raw[nb][j].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top = __vmaxu2(top, v[k] & 0x7FFF7FFFu);
-            }
-            top = max(top & 0xFFFFu, top >> 16);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = max((int)(top >> 7) - 127, -100);     // of the row's largest element
-            const float up = pow2f(13 - e);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const uint32_t v[4] = {raw[nb][j].x, raw[nb][j].y, raw[nb][j].z, raw[nb][j].w};
-                float x[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[2 * k] = __uint_as_float(v[k] << 16) * up;
-                    x[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u) * up;
-                }
-                if constexpr (CODES == CODES_INT4) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) qf[nb][j][k] = f16x2_rn(x[k], x[k + 4]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) qf[nb][j][k] = f16x2_rn(x[2 * k], x[2 * k + 1]);
-                }
-            }
-            const float f = A.scale_log2 * pow2f(e - 13);
-            fac[nb][0] = __shfl_sync(0xffffffffu, f, 8 * c);         // row 2c of the tile
-            fac[nb][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);     // row 2c + 1
-#pragma unroll
-            for (int h = 0; h < 2; ++h) lim[nb][h] = limit(min(row0 + 8 * nb + 2 * c + h, row0 + rows - 1));
+            for (int k = 0; k < 4; ++k) top = __vmaxu2(top, v[k] & 0x7FFF7FFFu);
         }
+        top = max(top & 0xFFFFu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max((int)(top >> 7) - 127, -100);     // of the row's largest element
+        const float up = pow2f(13 - e);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const uint32_t v[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = __uint_as_float(v[k] << 16) * up;
+                x[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u) * up;
+            }
+            if constexpr (CODES == CODES_INT4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) qf[j][k] = f16x2_rn(x[k], x[k + 4]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) qf[j][k] = f16x2_rn(x[2 * k], x[2 * k + 1]);
+            }
+        }
+        // (above zero, so that a masked -inf stays -inf)
+        const float f = fmaxf(A.scale_log2 * pow2f(e - 13), 1e-37f);
+        fac[0] = __shfl_sync(0xffffffffu, f, 8 * c);         // row 2c of the tile
+        fac[1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);     // row 2c + 1
+#pragma unroll
+        for (int h = 0; h < 2; ++h) lim[h] = limit(min(row0 + 2 * c + h, row0 + rows - 1));
 
-        float o[NB][NJ][2][4];
-        float m[NB][2], l[NB][2];
+        float o[NJ][2][4];
+        float m[2], l[2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[nb][j][k >> 2][k & 3] = 0.0f;
-            m[nb][0] = m[nb][1] = -INFINITY;
-            l[nb][0] = l[nb][1] = 0.0f;
-        }
+            for (int k = 0; k < 8; ++k) o[j][k >> 2][k & 3] = 0.0f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
         for (int it = 0; it < nt; ++it) {
             {
                 const int64_t row = row_next;
@@ -575,7 +568,7 @@ attend_split_kernel(const AttArgs A) {
                     for (int i = 0; i < Sw::N; ++i) v.w[i] = 0;
                 }
                 ev = max(__reduce_max_sync(0xffffffffu, v.template top<GS>()), -90);
-                const float down = pow2f(7 - ev);
+                const float down = pow2f(6 - ev);
 #pragma unroll
                 for (int g = 0; g < Sh::NG; ++g) {
                     const uint32_t h = f16x2_rn(v.template get<GS>(g) * down, 0.0f);
@@ -588,19 +581,17 @@ attend_split_kernel(const AttArgs A) {
                 __syncwarp();
             }
             // ---- scores
-            float sc[2][NB][4];
+            float sc[2][4];
 #pragma unroll
             for (int mb = 0; mb < 2; ++mb) {
                 const float *const sk = ks32 + mb * 16 + r;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[mb][nb][k] = 0.0f;
+                for (int k = 0; k < 4; ++k) sc[mb][k] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NJ; j += 2) {
                     uint32_t w[4];
                     ldsm4<false>(w, st_s + code_off<D>(mb * 16 + lm_t, j + lm_c));
-                    float acc[NB][4];
+                    float acc[4];
 #pragma unroll
                     for (int jj = 0; jj < 2; ++jj) {
                         uint32_t x[4], y[4];
@@ -611,123 +602,107 @@ attend_split_kernel(const AttArgs A) {
                             e2m1_bytes(w[2 * jj], x);
                             e2m1_bytes(w[2 * jj + 1], y);
                         }
+                        const uint32_t(&q)[4] = qf[j + jj];
+                        if constexpr (G == 16) {
+                            // lanes 0, 1 of a quad hold the first group's channels, 2, 3 the second's
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            const uint32_t(&q)[4] = qf[nb][j + jj];
-                            if constexpr (G == 16) {
-                                // lanes 0, 1 of a quad hold the first group's channels, 2, 3 the second's
+                            for (int half = 0; half < 2; ++half) {
+                                const bool on = (c >> 1) == half;
+                                const int g = 2 * (j + jj) + half;
+                                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma_f16(d, x[0], y[0], x[1], y[1], on ? q[0] : 0u, on ? q[1] : 0u);
+                                mma_f16(d, x[2], y[2], x[3], y[3], on ? q[2] : 0u, on ? q[3] : 0u);
+                                const float s0 = sk[g * kAttTile], s8 = sk[g * kAttTile + 8];
+                                sc[mb][0] = fmaf(d[0], s0, sc[mb][0]);
+                                sc[mb][1] = fmaf(d[1], s0, sc[mb][1]);
+                                sc[mb][2] = fmaf(d[2], s8, sc[mb][2]);
+                                sc[mb][3] = fmaf(d[3], s8, sc[mb][3]);
+                            }
+                        } else {
+                            if (G == 32 || jj == 0) {
 #pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    const bool on = (c >> 1) == half;
-                                    const int g = 2 * (j + jj) + half;
-                                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                    mma_f16(d, x[0], y[0], x[1], y[1], on ? q[0] : 0u, on ? q[1] : 0u);
-                                    mma_f16(d, x[2], y[2], x[3], y[3], on ? q[2] : 0u, on ? q[3] : 0u);
-                                    const float s0 = sk[g * kAttTile], s8 = sk[g * kAttTile + 8];
-                                    sc[mb][nb][0] = fmaf(d[0], s0, sc[mb][nb][0]);
-                                    sc[mb][nb][1] = fmaf(d[1], s0, sc[mb][nb][1]);
-                                    sc[mb][nb][2] = fmaf(d[2], s8, sc[mb][nb][2]);
-                                    sc[mb][nb][3] = fmaf(d[3], s8, sc[mb][nb][3]);
-                                }
-                            } else {
-                                if (G == 32 || jj == 0) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) acc[nb][k] = 0.0f;
-                                }
-                                mma_f16(acc[nb], x[0], y[0], x[1], y[1], q[0], q[1]);
-                                mma_f16(acc[nb], x[2], y[2], x[3], y[3], q[2], q[3]);
-                                if (G == 32 || jj == 1) {
-                                    const int g = (j + jj) * 32 / G;
-                                    const float s0 = sk[g * kAttTile], s8 = sk[g * kAttTile + 8];
-                                    sc[mb][nb][0] = fmaf(acc[nb][0], s0, sc[mb][nb][0]);
-                                    sc[mb][nb][1] = fmaf(acc[nb][1], s0, sc[mb][nb][1]);
-                                    sc[mb][nb][2] = fmaf(acc[nb][2], s8, sc[mb][nb][2]);
-                                    sc[mb][nb][3] = fmaf(acc[nb][3], s8, sc[mb][nb][3]);
-                                }
+                                for (int k = 0; k < 4; ++k) acc[k] = 0.0f;
+                            }
+                            mma_f16(acc, x[0], y[0], x[1], y[1], q[0], q[1]);
+                            mma_f16(acc, x[2], y[2], x[3], y[3], q[2], q[3]);
+                            if (G == 32 || jj == 1) {
+                                const int g = (j + jj) * 32 / G;
+                                const float s0 = sk[g * kAttTile], s8 = sk[g * kAttTile + 8];
+                                sc[mb][0] = fmaf(acc[0], s0, sc[mb][0]);
+                                sc[mb][1] = fmaf(acc[1], s0, sc[mb][1]);
+                                sc[mb][2] = fmaf(acc[2], s8, sc[mb][2]);
+                                sc[mb][3] = fmaf(acc[3], s8, sc[mb][3]);
                             }
                         }
                     }
                 }
             }
             // ---- softmax: the running maximum carries the exponent of the
-            // tiles' value scales (m is at least the largest score + exponent
-            // - 7 of every tile), p 2^E is what the products take
+            // tiles' value scales, p 2^E is what the products take.  It is
+            // raised, to the largest score + exponent - 7, only where that is
+            // more than 2 above it: p stays at most 2^9
             const bool cut = base + kAttTile > lim_min;
-            bool moved = false;
-            float alpha[NB][2], mu[NB][2];
+            float top[2];
+            bool raise = false;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
+            for (int h = 0; h < 2; ++h) {
+                float t = -INFINITY;
+#pragma unroll
+                for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float &x = sc[mb][2 * k + h];
+                        if (cut && base + mb * 16 + 8 * k + r >= lim[h]) x = -INFINITY;
+                        t = max_nan(t, x);
+                    }
+                top[h] = fmaf(t, fac[h], (float)(ev - 7));
+                raise |= top[h] > m[h] + 2.0f;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+                float alpha[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float t = -INFINITY;
-#pragma unroll
-                    for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float &x = sc[mb][nb][2 * k + h];
-                            x *= fac[nb][h];
-                            if (cut && base + mb * 16 + 8 * k + r >= lim[nb][h]) x = -INFINITY;
-                            t = max_nan(t, x);
-                        }
+                    float t = top[h];
                     t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 4));
                     t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 8));
                     t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    alpha[nb][h] = t;
+                    const float now = t > m[h] + 2.0f ? t : m[h];
+                    alpha[h] = now == m[h] ? 1.0f : ex2(m[h] - now);
+                    m[h] = now;
+                    l[h] *= alpha[h];
                 }
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[j][k >> 2][k & 3] *= alpha[k & 1];
             }
+            uint32_t pt[2][2];                              // transposed: tokens 2c, 2c + 1 (+ 8) of row r
+            float sum[2] = {0.0f, 0.0f}, off[2];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int h = 0; h < 2; ++h) off[h] = (float)ev - (m[h] == -INFINITY ? 0.0f : m[h]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float old = m[nb][h];
-                    const float now = max_nan(old, alpha[nb][h] + (float)(ev - 7));
-                    m[nb][h] = now;
-                    mu[nb][h] = now == -INFINITY ? 0.0f : now;
-                    alpha[nb][h] = ex2(old - mu[nb][h]);
-                    moved |= now != old;
+            for (int mb = 0; mb < 2; ++mb) {
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    p[k] = ex2(fmaf(sc[mb][k], fac[k & 1], off[k & 1]));
+                    sum[k & 1] += p[k];
                 }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    l[nb][0] *= alpha[nb][0];
-                    l[nb][1] *= alpha[nb][1];
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[nb][j][k >> 2][k & 3] *= alpha[nb][k & 1];
-                }
+                pt[mb][0] = movm(f16x2_rn(p[0], p[1]));
+                pt[mb][1] = movm(f16x2_rn(p[2], p[3]));
             }
-            uint32_t pt[2][NB][2];                              // transposed: tokens 2c, 2c + 1 (+ 8) of row r
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int mb = 0; mb < 2; ++mb) {
-                    float p[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        p[k] = ex2(sc[mb][nb][k] - (mu[nb][k & 1] - (float)ev));
-                        sum[k & 1] += p[k];
-                    }
-                    pt[mb][nb][0] = movm(f16x2_rn(p[0], p[1]));
-                    pt[mb][nb][1] = movm(f16x2_rn(p[2], p[3]));
-                }
-                const float up = pow2f(7 - ev);                 // (as the scales)
-                l[nb][0] = fmaf(sum[0], up, l[nb][0]);
-                l[nb][1] = fmaf(sum[1], up, l[nb][1]);
-            }
+            const float up = pow2f(6 - ev);                 // (as the scales)
+            l[0] = fmaf(sum[0], up, l[0]);
+            l[1] = fmaf(sum[1], up, l[1]);
             // ---- values
 #pragma unroll
             for (int mb = 0; mb < 2; ++mb) {
-                uint32_t p0[NB], p1[NB], p2[NB], p3[NB];        // B operands of the group(s) at hand
-                const auto probs = [&](int g, uint32_t(&b0)[NB], uint32_t(&b1)[NB]) {
+                uint32_t p0, p1, p2, p3;        // B operands of the group(s) at hand
+                const auto probs = [&](int g, uint32_t &b0, uint32_t &b1) {
                     const uint32_t *const s2 = reinterpret_cast<const uint32_t *>(vs16 + g * kAttTile + mb * 16);
                     const uint32_t s0 = s2[c], s8 = s2[c + 4];
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        b0[nb] = hmul2(pt[mb][nb][0], s0);
-                        b1[nb] = hmul2(pt[mb][nb][1], s8);
-                    }
+                    b0 = hmul2(pt[mb][0], s0);
+                    b1 = hmul2(pt[mb][1], s8);
                 };
 #pragma unroll
                 for (int j = 0; j < NJ; j += 2) {
@@ -754,14 +729,11 @@ attend_split_kernel(const AttArgs A) {
                         uint32_t x[4], y[4];
                         nibble_pairs<CODES>(wa, x, A.k16);
                         nibble_pairs<CODES>(wb, y, A.k16);
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            mma_f16(o[nb][j + jj][0], x[0], x[1], y[0], y[1], p0[nb], p1[nb]);
-                            if constexpr (G == 16)
-                                mma_f16(o[nb][j + jj][1], x[2], x[3], y[2], y[3], p2[nb], p3[nb]);
-                            else
-                                mma_f16(o[nb][j + jj][1], x[2], x[3], y[2], y[3], p0[nb], p1[nb]);
-                        }
+                        mma_f16(o[j + jj][0], x[0], x[1], y[0], y[1], p0, p1);
+                        if constexpr (G == 16)
+                            mma_f16(o[j + jj][1], x[2], x[3], y[2], y[3], p2, p3);
+                        else
+                            mma_f16(o[j + jj][1], x[2], x[3], y[2], y[3], p0, p1);
                     }
                 }
             }
@@ -772,27 +744,24 @@ attend_split_kernel(const AttArgs A) {
 
         // ---- join the warps
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int h = 0; h < 2; ++h) {
+            float t = l[h];
+            t += __shfl_xor_sync(0xffffffffu, t, 4);
+            t += __shfl_xor_sync(0xffffffffu, t, 8);
+            t += __shfl_xor_sync(0xffffffffu, t, 16);
+            const int row = 2 * c + h;
+            if (r == 0) join_ml[warp * ROWS + row] = make_float2(m[h], t);
+            float *const dst = join + (warp * ROWS + row) * Sh::OST;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float t = l[nb][h];
-                t += __shfl_xor_sync(0xffffffffu, t, 4);
-                t += __shfl_xor_sync(0xffffffffu, t, 8);
-                t += __shfl_xor_sync(0xffffffffu, t, 16);
-                const int row = 8 * nb + 2 * c + h;
-                if (r == 0) join_ml[warp * ROWS + row] = make_float2(m[nb][h], t);
-                float *const dst = join + (warp * ROWS + row) * Sh::OST;
+            for (int j = 0; j < NJ; ++j) {
+                if constexpr (G == 16) {
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    if constexpr (G == 16) {
-#pragma unroll
-                        for (int blk = 0; blk < 2; ++blk)
-                            *reinterpret_cast<float2 *>(dst + 32 * j + 16 * blk + 4 * (r & 3) + 2 * (r >> 2)) =
-                                make_float2(o[nb][j][blk][h], o[nb][j][blk][2 + h]);
-                    } else {
-                        *reinterpret_cast<float4 *>(dst + 32 * j + 4 * r) =
-                            make_float4(o[nb][j][0][h], o[nb][j][0][2 + h], o[nb][j][1][h], o[nb][j][1][2 + h]);
-                    }
+                    for (int blk = 0; blk < 2; ++blk)
+                        *reinterpret_cast<float2 *>(dst + 32 * j + 16 * blk + 4 * (r & 3) + 2 * (r >> 2)) =
+                            make_float2(o[j][blk][h], o[j][blk][2 + h]);
+                } else {
+                    *reinterpret_cast<float4 *>(dst + 32 * j + 4 * r) =
+                        make_float4(o[j][0][h], o[j][0][2 + h], o[j][1][h], o[j][1][2 + h]);
                 }
             }
         }
@@ -851,11 +820,11 @@ attend_split_kernel(const AttArgs A) {
 // Joins the pieces of the segments that were cut: CTA (i, row) takes the one
 // that starts in share i.  Four warps take every fourth piece each; their
 // sums are added in a fixed order.
-template <int D, int NB>
+template <int D>
 __global__ void __launch_bounds__(128)
 attend_join_kernel(const AttArgs A, int n) {
     grid_dependency_begin();
-    constexpr int ROWS = 8 * NB;
+    constexpr int ROWS = 8;
     __shared__ float4 s_acc[4][D / 4];
     __shared__ float s_sum[4];
     const AttMeta mt = A.meta[blockIdx.x];
@@ -942,11 +911,11 @@ inline AttArgs att_args(const AttendLaunch &L, int slots, int rows, int few) {
     return A;
 }
 
-template <int CODES, int GS, int G, int D, int NB>
+template <int CODES, int GS, int G, int D>
 cudaError_t launch_attend_split(AttendLaunch &L, int few) {
-    using Sh = AttShape<CODES, GS, G, D, NB>;
+    using Sh = AttShape<CODES, GS, G, D>;
     const AttArgs A = att_args(L, 2 * kAttCtas, Sh::ROWS, few);
-    const auto kern = attend_split_kernel<CODES, GS, G, D, NB>;
+    const auto kern = attend_split_kernel<CODES, GS, G, D>;
     static std::atomic<bool> done[64];
     cudaError_t e = smem_opt_in(kern, Sh::BYTES, done);
     if (e != cudaSuccess) return e;
@@ -956,7 +925,7 @@ cudaError_t launch_attend_split(AttendLaunch &L, int few) {
     // (sequences of at most one unit are never cut)
     if ((int64_t)L.batch.max_pages * L.cache.page_size <= kAttUnit) return cudaSuccess;
     L.launches += 1;
-    return launch_k(attend_join_kernel<D, NB>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
+    return launch_k(attend_join_kernel<D>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
 }
 
 }  // namespace dq

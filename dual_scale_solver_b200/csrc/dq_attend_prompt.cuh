@@ -801,7 +801,7 @@ cudaError_t launch_attend_d(AttendLaunch &L) {
     cudaError_t e = cudaSuccess;
     if (by & ATT_MANY) e = launch_attend_prompt<CODES, GS, G, D>(L, by & ATT_FEW ? kAttFew : 0);
     if (e != cudaSuccess || !(by & ATT_FEW)) return e;
-    return launch_attend_split<CODES, GS, G, D, 1>(L, by & ATT_MANY ? kAttFew : INT32_MAX);
+    return launch_attend_split<CODES, GS, G, D>(L, by & ATT_MANY ? kAttFew : INT32_MAX);
 }
 
 template <int CODES, int GS>

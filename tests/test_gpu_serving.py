@@ -214,8 +214,9 @@ def _check_attention(B, q, cache, values, scale=None, causal=True, out=None, **k
     2^-23) A scale, A = the row's largest sum |q k|, which moves every weight
     by that twice (its own and the sum's).  Last, fp16's absolute step, half
     of it 2^-25 below 2^-14.  With 2^E <= S, S the largest value scale: for
-    few rows the operand is p s 2^(14 - E) against a sum of at least one 2^(14
-    - E), times a code of at most 8: 2^-36 S for each position; for prompts
+    few rows the operand is p s 2^(13 - E) against a sum of at least one 2^(13
+    - E), times a code of at most 8: 2^-35 S for each position (and p itself,
+    2^(7 .. 9) times a scale of at most 2^7: 2^-28 S); for prompts
     it is p 2^(E + 7 .. 15) against a sum that holds the row's largest of
     them, 2^7, times 2^-E, multiplied by code x scale / 2^E of at most 16:
     2^-28 S."""
@@ -310,6 +311,33 @@ def test_attention_prompts_many_sequences():
         cache, values = B.fill()
         q = bf16_from(B.rng, (B.tokens, 8, 64)).cuda()
         _check_attention(B, q, cache, values)
+
+
+@pytest.mark.parametrize("name,G", [("int4_bf16", 64), ("mxfp4", 32)])
+@pytest.mark.parametrize("seqs,group", [([(1, 300)] * 40 + [(100, 500), (32, 700)], 2),      # 7 rows in the mean
+                                        ([(1, 900), (600, 1300), (4, 50), (0, 9), (9, 40), (8, 3)], 4),
+                                        ([(1, 600), (1, 5), (3, 3)], 48)])
+def test_attention_mixed_batches(name, G, seqs, group):
+    """Single tokens, drafts and prompts in one call: sequences of up to 32
+    rows and longer ones."""
+    B = Batch(seqs, 16, 2, 64, name, G, pad=2)
+    cache, values = B.fill()
+    q = bf16_from(B.rng, (B.tokens, 2 * group, 64)).cuda()
+    out = torch.full_like(q, 5.0)
+    for causal in (True, False):
+        a = _check_attention(B, q, cache, values, causal=causal, out=out).clone()
+        assert bool((a[int(B.starts[-1]):] == 5.0).all())
+
+
+@pytest.mark.parametrize("length", [-1, 65, 0x7FFFFFFF])
+def test_bad_length_of_a_lone_prompt(length):
+    cache = dq.kv_cache(5, 16, 1, 64, dq.format_preset("mxfp4"))
+    q = torch.ones(40, 4, 64, dtype=torch.bfloat16, device="cuda")
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.full_like(q, 5.0)
+    table = i(0, 1, 2, 3).view(1, 4)
+    dq.kv_attention(q, cache, i(0, 40), i(length), table, dq.format_preset("mxfp4"), out=out)
+    assert dq.last_device_status() == -12 and bool((out == 5.0).all())
 
 
 @pytest.mark.parametrize("name,G", [("int4_bf16", 64), ("nvfp4_ts1", 16)])
