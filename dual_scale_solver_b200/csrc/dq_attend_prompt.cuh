@@ -32,6 +32,16 @@
 //                    codes in registers while the previous tile is expanded
 //   warps 12, 13     issue the MMAs of row tile 0, 1
 // Every wait is bounded (dq_tc.cuh).
+//
+// Scores are taken in steps of 64 positions, two steps' columns in turn, so
+// that the products of one step run during the softmax of the next (one step
+// of 128: 1.13 against 1.07 ms).  Measured (64 query over 8 cache heads, D =
+// 128, NVFP4): 2 sequences of 1000 new tokens over 16384 positions 980 us, 1.01
+// PFLOP/s; 2048 new tokens alone (32 query heads, MXFP4) 58 us, 0.6 PFLOP/s.
+// Scores 64 columns wide run at two thirds of the tensor core's rate, so the
+// products fill 55% of its time; exponentials fill 44% of theirs.  More warps
+// (eight that expand codes, or two softmax teams) were slower, 1.2 ms: the
+// registers a thread keeps fall below 96.
 #pragma once
 
 #include "dq_attend.cuh"
@@ -388,16 +398,19 @@ attend_prompt_kernel(const AttArgs A, int split) {
                 // this row of Q, as fp16 scaled so that its largest element is in [2^13, 2^14)
                 uint32_t top = 0;
                 const uint4 *src = reinterpret_cast<const uint4 *>(A.q + qrow * A.q_token + qhead * A.q_head);
-#pragma unroll 4
+                uint4 raw[D / 8];                               // (in the registers that scores take later)
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) raw[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    const uint4 v = raw[i];
                     top = __vmaxu2(__vmaxu2(top, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
                 }
                 const int e = max((int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, -100);
                 const float up = pow2f(13 - e);
-#pragma unroll 4
+#pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    const uint4 v = raw[i];
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     float x[8];
 #pragma unroll
@@ -520,15 +533,21 @@ attend_prompt_kernel(const AttArgs A, int split) {
                 const int slot = 2 * (int)blockIdx.x + (it.t0 == 0 ? 1 : 0), prow = 128 * t + row_in;
                 float4 *const dst = reinterpret_cast<float4 *>(A.part) + (int64_t)slot * (D / 4) * kPromptRows + prow;
                 if ((warp & 3) * 32 < it.rows[t]) {
-#pragma unroll 2
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                        if (nt > 0) tc::tmem_load8(o_addr + 8 * c, o);
-                        float y[8];
+#pragma unroll 1
+                    for (int b = 0; b < D / 32; ++b) {
+                        uint32_t o[32];
+                        tc::tmem_load(o_addr + 32 * b, o);      // (anything where nt is 0)
+                        tc::tmem_load_wait(o);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) y[prompt_order<CODES>(k)] = __uint_as_float(o[k]) * pow2f(-kPromptK0);
-                        dst[(2 * c) * kPromptRows] = make_float4(y[0], y[1], y[2], y[3]);
-                        dst[(2 * c + 1) * kPromptRows] = make_float4(y[4], y[5], y[6], y[7]);
+                        for (int c = 0; c < 4; ++c) {
+                            float y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                y[prompt_order<CODES>(k)] =
+                                    nt > 0 ? __uint_as_float(o[8 * c + k]) * pow2f(-kPromptK0) : 0.0f;
+                            dst[(8 * b + 2 * c) * kPromptRows] = make_float4(y[0], y[1], y[2], y[3]);
+                            dst[(8 * b + 2 * c + 1) * kPromptRows] = make_float4(y[4], y[5], y[6], y[7]);
+                        }
                     }
                     A.part_ml[slot * kPromptRows + prow] = make_float2(m, l);
                 }
@@ -550,20 +569,22 @@ attend_prompt_kernel(const AttArgs A, int split) {
             } else if (it.rows[t] > 0) {
                 const float inv = l == 0.0f ? 0.0f : pow2f(-kPromptK0) / l;      // (l is NaN where Q is)
                 uint16_t *const dst = A.out + qrow * A.out_token + qhead * A.out_head;
-#pragma unroll 2
-                for (int c = 0; c < D / 8; ++c) {
-                    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (nt > 0) tc::tmem_load8(o_addr + 8 * c, o);
-                    if (valid) {
+#pragma unroll 1
+                for (int b = 0; b < D / 32; ++b) {
+                    uint32_t o[32];
+                    tc::tmem_load(o_addr + 32 * b, o);          // (anything where nt is 0)
+                    tc::tmem_load_wait(o);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
                         float y[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            y[prompt_order<CODES>(k)] = inv == 0.0f ? 0.0f : __uint_as_float(o[k]) * inv;
+                            y[prompt_order<CODES>(k)] = inv == 0.0f ? 0.0f : __uint_as_float(o[8 * c + k]) * inv;
                         uint32_t h[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(y[2 * k + 1]), "f"(y[2 * k]));
-                        *reinterpret_cast<uint4 *>(dst + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+                        if (valid) *reinterpret_cast<uint4 *>(dst + 32 * b + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
                 tc::fence_before();                 // (these reads before the next item's products)

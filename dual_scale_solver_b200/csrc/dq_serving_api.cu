@@ -64,6 +64,7 @@ dq_status kv_copy(const void *k, int64_t k_token, int64_t k_head, const void *v,
     if (tokens == 0 || batch->seqs == 0) return DQ_OK;
     if ((s = check_rows(k, k_token, k_head, tokens, cache->heads, cache->head_dim, read)) != DQ_OK) return s;
     if ((s = check_rows(v, v_token, v_head, tokens, cache->heads, cache->head_dim, read)) != DQ_OK) return s;
+    if (read && k == v) return DQ_ERR_ARG;
     KvCopyLaunch L;
     L.status = serving_status_word();
     if (!L.status) return DQ_ERR_CUDA;
@@ -169,6 +170,7 @@ dq_status dq_kv_attention(const void *q, int64_t q_token, int64_t q_head, void *
         ws_bytes < attend_workspace(tokens, q_heads, cache->heads, cache->head_dim, batch->seqs))
         return DQ_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return DQ_ERR_ALIGN;
+    if (out == q) return DQ_ERR_ARG;             // (rows of q are read until the call's end)
     AttendLaunch L;
     L.status = serving_status_word();
     if (!L.status) return DQ_ERR_CUDA;

@@ -53,19 +53,6 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile 
     return false;
 }
 
-// ---- named barriers of some warps (every thread of them arrives)
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("barrier.cta.sync.aligned %0, %1;" :: "r"(id), "r"(threads) : "memory");
-}
-// whether the predicate holds in any of the threads
-__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
-    uint32_t r;
-    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %3, 0;\n\t"
-                 "barrier.cta.red.or.pred.aligned q, %1, %2, p; selp.u32 %0, 1, 0, q; }"
-                 : "=r"(r) : "r"(id), "r"(threads), "r"((uint32_t)v) : "memory");
-    return r != 0;
-}
-
 // ---- ordering
 __device__ __forceinline__ void fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -122,12 +109,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 
 // ---- TMEM: 32 consecutive 32-bit columns of this thread's lane
-#define DQ_TC_R32(r)                                                                                   \
-    "r"((r)[0]), "r"((r)[1]), "r"((r)[2]), "r"((r)[3]), "r"((r)[4]), "r"((r)[5]), "r"((r)[6]),         \
-        "r"((r)[7]), "r"((r)[8]), "r"((r)[9]), "r"((r)[10]), "r"((r)[11]), "r"((r)[12]), "r"((r)[13]), \
-        "r"((r)[14]), "r"((r)[15]), "r"((r)[16]), "r"((r)[17]), "r"((r)[18]), "r"((r)[19]),            \
-        "r"((r)[20]), "r"((r)[21]), "r"((r)[22]), "r"((r)[23]), "r"((r)[24]), "r"((r)[25]),            \
-        "r"((r)[26]), "r"((r)[27]), "r"((r)[28]), "r"((r)[29]), "r"((r)[30]), "r"((r)[31])
 #define DQ_TC_W32(c, r)                                                                                \
     c((r)[0]), c((r)[1]), c((r)[2]), c((r)[3]), c((r)[4]), c((r)[5]), c((r)[6]), c((r)[7]), c((r)[8]), \
         c((r)[9]), c((r)[10]), c((r)[11]), c((r)[12]), c((r)[13]), c((r)[14]), c((r)[15]),             \
@@ -144,13 +125,6 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
 // the registers of earlier loads are valid after it (and not used before it)
 __device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : DQ_TC_W32("+r", r) :: "memory");
-}
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
-        :: DQ_TC_R32(r), "r"(addr) : "memory");
 }
 // 8 columns
 __device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t (&r)[8]) {
@@ -178,14 +152,6 @@ __device__ __forceinline__ void tmem_alloc(uint32_t *base) {
 template <uint32_t COLS>
 __device__ __forceinline__ void tmem_free(uint32_t base) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(base), "r"(COLS) : "memory");
-}
-
-// ---- registers of a warpgroup
-template <int N> __device__ __forceinline__ void regs_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
-}
-template <int N> __device__ __forceinline__ void regs_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
 
 }  // namespace tc

@@ -105,6 +105,7 @@ def test_cache_copy_refusals(which):
         assert _copy(which, **kw) == status, kw
     # rows that are written may not overlap; rows that are read may
     if which == "dq_kv_read":
+        assert _copy(which) == -1                                  # both over each other
         assert _copy(which, kt=128) == -2 and _copy(which, kh=64) == -2 and _copy(which, vt=0) == -2
 
 
@@ -126,6 +127,7 @@ def test_attention_refusals():
     assert _attend(causal=2) == -1
     assert _attend(q=None) == -1 and _attend(out=None) == -1
     assert _attend(q=ODD) == -9 and _attend(out=ODD) == -9
+    assert _attend() == -1                                         # out over q
     assert _attend(ot=256) == -2 and _attend(oh=0) == -2 and _attend(qh=12) == -2
     assert _attend(ws=None) == -7 and _attend(bytes_=1024) == -7
     assert _attend(ws=ctypes.c_void_p(4096 + 16)) == -9
