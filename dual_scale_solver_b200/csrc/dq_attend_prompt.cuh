@@ -36,8 +36,8 @@
 // Scores are taken in steps of 64 positions, two steps' columns in turn, so
 // that the products of one step run during the softmax of the next (one step
 // of 128: 1.13 against 1.07 ms).  Measured (64 query over 8 cache heads, D =
-// 128, NVFP4): 2 sequences of 1000 new tokens over 16384 positions 980 us, 1.01
-// PFLOP/s; 2048 new tokens alone (32 query heads, MXFP4) 58 us, 0.6 PFLOP/s.
+// 128, NVFP4): 2 sequences of 1000 new tokens over 16384 positions 971 us, 1.02
+// PFLOP/s; 2048 new tokens alone (32 query heads, MXFP4) 54 us, 0.63 PFLOP/s.
 // Scores 64 columns wide run at two thirds of the tensor core's rate, so the
 // products fill 55% of its time; exponentials fill 44% of theirs.  More warps
 // (eight that expand codes, or two softmax teams) were slower, 1.2 ms: the

@@ -10,8 +10,8 @@
 //
 // Moves 2 bytes per channel in (or out) and half a byte of codes.  16
 // sequences of 2048 new tokens, 8 heads of 128, MXFP4: append 40 us, read 38
-// (3.7 TB/s): the append is bound by the quantizer's instructions (NVFP4,
-// whose scales are divided by, 95 us), the read by its 4-byte loads of codes.
+// (3.7 TB/s): both are bound by instructions (issue 66% in the read), the
+// append by the quantizer's (NVFP4, whose scales are divided by, 95 us).
 #include <cuda_runtime.h>
 
 #include "dq_kv.cuh"
