@@ -9,9 +9,9 @@
 // starts at a time) and then walks the heads of keys and values.
 //
 // Moves 2 bytes per channel in (or out) and half a byte of codes.  16
-// sequences of 2048 new tokens, 8 heads of 128, MXFP4: append 40 us, read 38
-// (3.7 TB/s): both are bound by instructions (issue 66% in the read), the
-// append by the quantizer's (NVFP4, whose scales are divided by, 95 us).
+// sequences of 2048 new tokens, 8 heads of 128, MXFP4: append 35 us (4.2 TB/s,
+// bound by the quantizer's instructions; NVFP4, whose scales are divided by,
+// 89), read 31 (4.8 TB/s).
 #include <cuda_runtime.h>
 
 #include "dq_kv.cuh"
@@ -63,46 +63,38 @@ kv_copy_kernel(const KvCopyArgs A) {
             if (lane == 0) atomicOr(A.status, STATUS_INDEX);
             if (!READ) continue;
         }
-        const int rows = 2 * A.cache.heads;             // keys, then values
-        // UN steps at a time, their loads first: a warp's rows are few, and
-        // one load after the other would leave the memory idle (at the size
-        // above: one step 52 us, two 40, four 41 to 44, eight 49)
-        constexpr int UN = 2;
-        const int hop = A.splits * RPW;
-        for (int r0 = part * RPW; r0 < rows; r0 += UN * hop) {
-            uint16_t *x[UN];
-            uint8_t *codes[UN];
-            void *scales[UN];
-            int64_t gi[UN];
-            bool ok[UN];
-            uint4 in[UN];
-            float sc[UN];
-            const int c = lane % LPR;
+        // a head's key and value row together: their places differ by the
+        // arrays' addresses only, and both loads are under way at once
+        const int c = lane % LPR, heads = A.cache.heads, hop = A.splits * RPW;
+        const int h0 = part * RPW;                      // (the warp's first head; a lane's is up to RPW - 1 more)
+        const int64_t row = row0 + (int64_t)(h0 + lane / LPR) * A.cache.page_size;
+        int64_t co = row * (D / 2) + 4 * c, so = row * (D / G) + c / (G / 8);
+        const int64_t co_hop = (int64_t)hop * A.cache.page_size * (D / 2);
+        const int64_t so_hop = (int64_t)hop * A.cache.page_size * (D / G);
+        uint16_t *x[2] = {A.k + t * A.k_token + (h0 + lane / LPR) * A.k_head + 8 * c,
+                          A.v + t * A.v_token + (h0 + lane / LPR) * A.v_head + 8 * c};
+        const int64_t x_hop[2] = {hop * A.k_head, hop * A.v_head};
+        uint8_t *const codes[2] = {A.cache.k_codes, A.cache.v_codes};
+        void *const scales[2] = {A.cache.k_scales, A.cache.v_scales};
+        for (int h = h0; h < heads; h += hop, co += co_hop, so += so_hop, x[0] += x_hop[0], x[1] += x_hop[1]) {
+            const bool ok = h + lane / LPR < heads;
+            uint4 in[2];
+            float sc[2];
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                const int r = r0 + i * hop + lane / LPR;
-                ok[i] = r < rows;
-                const bool val = r >= A.cache.heads;
-                const int head = ok[i] ? (val ? r - A.cache.heads : r) : 0;
-                x[i] = (val ? A.v + t * A.v_token + head * A.v_head : A.k + t * A.k_token + head * A.k_head) + 8 * c;
-                const int64_t row = row0 + (int64_t)head * A.cache.page_size;
-                codes[i] = (val ? A.cache.v_codes : A.cache.k_codes) + row * (D / 2) + 4 * c;
-                scales[i] = val ? A.cache.v_scales : A.cache.k_scales;
-                gi[i] = row * (D / G) + c / (G / 8);
+            for (int i = 0; i < 2; ++i) {
                 in[i] = make_uint4(0, 0, 0, 0);
                 sc[i] = 0.0f;
                 if constexpr (READ) {
-                    if (ok[i] && row0 >= 0) {
-                        in[i].x = *reinterpret_cast<const uint32_t *>(codes[i]);
-                        sc[i] = scale_value<GS>(scales[i], gi[i]);
+                    if (ok && row0 >= 0) {
+                        in[i].x = *reinterpret_cast<const uint32_t *>(codes[i] + co);
+                        sc[i] = scale_value<GS>(scales[i], so);
                     }
                 } else {
-                    if (ok[i]) in[i] = __ldg(reinterpret_cast<const uint4 *>(x[i]));
+                    if (ok) in[i] = __ldg(reinterpret_cast<const uint4 *>(x[i]));
                 }
             }
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                if (r0 + i * hop >= rows) break;        // (the whole warp)
+            for (int i = 0; i < 2; ++i) {
                 if constexpr (READ) {
                     uint32_t p[4];
 #pragma unroll
@@ -114,7 +106,7 @@ kv_copy_kernel(const KvCopyArgs A) {
                                              : e2m1x2_to_f32(b);
                         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[k]) : "f"(v.y * sc[i]), "f"(v.x * sc[i]));
                     }
-                    if (ok[i]) *reinterpret_cast<uint4 *>(x[i]) = make_uint4(p[0], p[1], p[2], p[3]);
+                    if (ok) *reinterpret_cast<uint4 *>(x[i]) = make_uint4(p[0], p[1], p[2], p[3]);
                 } else {
                     Chunk<Bf16Tag> ch;
                     ch.raw = in[i];
@@ -125,15 +117,15 @@ kv_copy_kernel(const KvCopyArgs A) {
                     bool nonzero;
                     Quant<CODES, GS, SC_BF16, true, 4, G / 8>::template run<true>(
                         z, z, 1.0f, 1.0f, z, 1.0f, 1.0f, A.status, code, s, s_eff, cw, nonzero, mbits);
-                    if (!ok[i]) continue;
-                    *reinterpret_cast<uint32_t *>(codes[i]) = cw[0];
+                    if (!ok) continue;
+                    *reinterpret_cast<uint32_t *>(codes[i] + co) = cw[0];
                     if (c % (G / 8) == 0) {
                         if constexpr (GS == SC_BF16)
-                            reinterpret_cast<uint16_t *>(scales[i])[gi[i]] = (uint16_t)(__float_as_uint(s) >> 16);
+                            static_cast<uint16_t *>(scales[i])[so] = (uint16_t)(__float_as_uint(s) >> 16);
                         else if constexpr (GS == SC_E8M0)
-                            reinterpret_cast<uint8_t *>(scales[i])[gi[i]] = (uint8_t)(__float_as_uint(s) >> 23);
+                            static_cast<uint8_t *>(scales[i])[so] = (uint8_t)(__float_as_uint(s) >> 23);
                         else
-                            reinterpret_cast<uint8_t *>(scales[i])[gi[i]] = (uint8_t)e4m3_bits(s);
+                            static_cast<uint8_t *>(scales[i])[so] = (uint8_t)e4m3_bits(s);
                     }
                 }
             }
@@ -156,7 +148,7 @@ cudaError_t launch_fmt(const KvCopyLaunch &L) {
     A.status = L.status;
     // A token's rows are shared by as many warps as it takes to give every SM
     // 16 of them; a warp per token where there are more (fewer lookups).
-    const int steps = (2 * L.cache.heads * (L.cache.head_dim / 8) + 31) / 32;
+    const int steps = (L.cache.heads * (L.cache.head_dim / 8) + 31) / 32;
     int splits = 1;
     while (splits < steps && L.tokens * splits < 148 * 16) splits *= 2;
     A.splits = splits;
