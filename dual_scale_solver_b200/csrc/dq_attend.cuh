@@ -50,7 +50,13 @@ namespace dq {
 constexpr int kAttWarps = 8;
 constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kAttTile = 32;                       // tokens per warp step
-constexpr int kAttUnit = kAttTile * kAttWarps;     // tokens per unit
+constexpr int kAttUnit = kAttTile * kAttWarps;     // tokens per step of a CTA, and per unit of work;
+// but where every sequence has at most this many steps, segments are whole: a
+// step takes about 1 us, writing and joining pieces 5.  One token, us, cut
+// against whole: 511 positions 10.1, 7.4 (8 heads of 128) and 12.0, 6.3 (3 of
+// 64); 1000 11.1, 10.3; 32 sequences 17.0, 13.7; 48 23.4, 23.6; 128 47.7, 45.4; 2000
+// positions 12.8, 16.0; 32 sequences 23.7, 23.0; 128 67.6, 75.5.
+constexpr int kAttWhole = 4;
 constexpr int kAttCtas = 2 * 148;
 
 // Sequences of up to 32 query rows (new tokens x heads of a group) are this
@@ -111,11 +117,11 @@ struct AttSpan {            // a sequence's segments and units
 };
 
 template <int ROWS>
-__device__ __forceinline__ AttSpan att_span(const AttArgs &A, const KvSeq &s) {
+__device__ __forceinline__ AttSpan att_span(const AttArgs &A, const KvSeq &s, int unit) {
     AttSpan a;
     const long long rows = (long long)s.n * A.group;
     a.qt = rows > A.few ? 0 : (int)((rows + ROWS - 1) / ROWS);
-    a.kvt = max(1, (s.len + kAttUnit - 1) / kAttUnit);
+    a.kvt = max(1, (s.len + unit - 1) / unit);
     a.units = (long long)a.qt * A.cache.heads * a.kvt;
     return a;
 }
@@ -345,11 +351,17 @@ attend_split_kernel(const AttArgs A) {
     const int heads = A.cache.heads, seqs = A.batch.seqs;
 
     // ---- this CTA's share: units [u0, u1) of the batch
-    long long mine = 0, total = 0;
+    bool longer = false;
     for (int b = tid; b < seqs; b += kAttThreads) {
         const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
         if (!s.ok && me == 0) atomicOr(A.status, STATUS_INDEX);
-        mine = att_span<ROWS>(A, s).units;
+        longer |= s.len > kAttWhole * kAttUnit;
+    }
+    const int unit = __syncthreads_or(longer) ? kAttUnit : kAttWhole * kAttUnit;
+    long long mine = 0, total = 0;
+    for (int b = tid; b < seqs; b += kAttThreads) {
+        const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
+        mine = att_span<ROWS>(A, s, unit).units;
         total += mine;
     }
     const auto block_scan = [&](long long v, long long &all) {     // inclusive
@@ -389,7 +401,7 @@ attend_split_kernel(const AttArgs A) {
         for (int b0 = 0; b0 < seqs; b0 += kAttThreads) {
             const int b = b0 + tid;
             long long v = 0, all;
-            if (b < seqs) v = att_span<ROWS>(A, kv_seq(A.batch, A.cache.page_size, A.tokens, b)).units;
+            if (b < seqs) v = att_span<ROWS>(A, kv_seq(A.batch, A.cache.page_size, A.tokens, b), unit).units;
             const long long in = base + block_scan(v, all);
             if (v > 0 && in - v <= u0 && u0 < in) {
                 s_seq = b;
@@ -413,7 +425,7 @@ attend_split_kernel(const AttArgs A) {
 
     for (long long u = u0; u < u1;) {
         const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, seq);
-        const AttSpan sp = att_span<ROWS>(A, s);
+        const AttSpan sp = att_span<ROWS>(A, s, unit);
         if (u >= first + sp.units) {
             first += sp.units;
             ++seq;
@@ -431,7 +443,7 @@ attend_split_kernel(const AttArgs A) {
             return A.causal ? min(max(s.len - s.n + row / A.group + 1, 0), s.len) : s.len;
         };
         const int lim_min = limit(row0), lim_max = limit(row0 + rows - 1);
-        const int lo = t0 * kAttUnit, hi = min(t1 * kAttUnit, lim_max);
+        const int lo = t0 * unit, hi = min(t1 * unit, lim_max);
 
         // ---- tokens, 32 at a time; the first loads go out before anything else
         const int base0 = lo + kAttTile * warp;
@@ -931,8 +943,8 @@ cudaError_t launch_attend_split(AttendLaunch &L, int few) {
     e = launch_k(kern, dim3(kAttCtas), dim3(kAttThreads), Sh::BYTES, L.stream, A);
     if (e != cudaSuccess) return e;
     L.launches += 1;
-    // (sequences of at most one unit are never cut)
-    if ((int64_t)L.batch.max_pages * L.cache.page_size <= kAttUnit) return cudaSuccess;
+    // (nothing is cut where no sequence can be longer)
+    if ((int64_t)L.batch.max_pages * L.cache.page_size <= kAttWhole * kAttUnit) return cudaSuccess;
     L.launches += 1;
     return launch_k(attend_join_kernel<D>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
 }
