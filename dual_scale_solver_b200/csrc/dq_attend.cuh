@@ -83,13 +83,11 @@ inline int attend_kernels(int64_t tokens, int32_t q_heads, int32_t heads, int32_
 // What CTA i leaves for the joining kernel: the segment that starts (and
 // does not end) in its share.
 struct AttMeta {
-    long long units;        // units of the whole batch
     int last;               // the last share with a piece of the segment
     int rows;               // of the segment; 0: nothing to join
     int row0;               // its first row in the sequence
     int head;
     int token0;             // the sequence's first token row
-    int pad;
 };
 
 struct AttArgs {
@@ -348,7 +346,7 @@ attend_split_kernel(const AttArgs A) {
     __shared__ int s_seq;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
-    const int n = gridDim.x, me = blockIdx.x;
+    const int me = blockIdx.x;
     const int heads = A.cache.heads, seqs = A.batch.seqs;
 
     // ---- this CTA's share: units [u0, u1) of the batch
@@ -384,14 +382,10 @@ attend_split_kernel(const AttArgs A) {
         return v + before;
     };
     long long units, incl = block_scan(total, units);
+    if (tid == 0) A.meta[me] = AttMeta{};
+    const int n = (int)min((long long)gridDim.x, units);       // shares, none of them empty
+    if (me >= n) return;
     const long long u0 = units * me / n, u1 = units * (me + 1) / n;
-    if (tid == 0) {
-        AttMeta m;
-        m.units = units;
-        m.last = m.rows = m.row0 = m.head = m.token0 = m.pad = 0;
-        A.meta[me] = m;
-    }
-    if (u0 >= u1) return;
     if (seqs <= kAttThreads) {
         if (tid < seqs && incl - mine <= u0 && u0 < incl) {
             s_seq = tid;
@@ -825,13 +819,11 @@ attend_split_kernel(const AttArgs A) {
         if (!whole && t0 == 0 && tid == 0) {
             const long long end = first + (long long)(seg + 1) * sp.kvt;    // (its last unit, plus 1)
             AttMeta mt;
-            mt.units = units;
             mt.last = (int)min((long long)n - 1, (end * n - 1) / units);
             mt.rows = rows;
             mt.row0 = row0;
             mt.head = head;
             mt.token0 = s.s0;
-            mt.pad = 0;
             A.meta[me] = mt;
         }
         __syncthreads();
@@ -844,7 +836,7 @@ attend_split_kernel(const AttArgs A) {
 // sums are added in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(128)
-attend_join_kernel(const AttArgs A, int n) {
+attend_join_kernel(const AttArgs A) {
     grid_dependency_begin();
     constexpr int ROWS = 8;
     __shared__ float4 s_acc[4][D / 4];
@@ -852,17 +844,12 @@ attend_join_kernel(const AttArgs A, int n) {
     const AttMeta mt = A.meta[blockIdx.x];
     const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (row >= mt.rows) return;
-    // shares i, i + 1, ..., last hold pieces (empty shares hold none)
+    // shares i, i + 1, ..., last hold pieces
     const int i0 = blockIdx.x, last = mt.last;
-    const auto piece = [&](int i) {             // slot, or -1
-        if (mt.units < n && i > i0 && mt.units * i / n >= mt.units * (i + 1) / n) return -1;
-        return 2 * i + (i == i0 ? 1 : 0);
-    };
+    const auto piece = [&](int i) { return 2 * i + (i == i0 ? 1 : 0); };     // its slot
     float mx = -INFINITY;
-    for (int i = i0 + lane; i <= last; i += 32) {
-        const int k = piece(i);
-        if (k >= 0) mx = max_nan(mx, A.part_ml[k * ROWS + row].x);
-    }
+    for (int i = i0 + lane; i <= last; i += 32)
+        mx = max_nan(mx, A.part_ml[piece(i) * ROWS + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float base = mx == -INFINITY ? 0.0f : mx;
@@ -871,7 +858,6 @@ attend_join_kernel(const AttArgs A, int n) {
 #pragma unroll 4
     for (int i = i0 + warp; i <= last; i += 4) {
         const int k = piece(i);
-        if (k < 0) continue;
         const float2 ml = A.part_ml[k * ROWS + row];
         const float f = ex2(ml.x - base);
         sum = fmaf(ml.y, f, sum);
@@ -947,7 +933,7 @@ cudaError_t launch_attend_split(AttendLaunch &L, int few) {
     // (nothing is cut where no sequence can be longer)
     if ((int64_t)L.batch.max_pages * L.cache.page_size <= kAttWhole * kAttUnit) return cudaSuccess;
     L.launches += 1;
-    return launch_k(attend_join_kernel<D>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A, kAttCtas);
+    return launch_k(attend_join_kernel<D>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A);
 }
 
 }  // namespace dq

@@ -287,13 +287,14 @@ __device__ __forceinline__ void prompt_plan(const AttArgs &A, Smem &sm, int warp
     const long long units = sm.plan_units, items = sm.plan_items;
     if (items == 0 || (items + n - 1) / n * units * n <= items * (units + (long long)kPromptJoin * n)) return;
     // the place of unit u0, by one thread of each warp for its own walk
-    const long long u0 = units * blockIdx.x / n, u1 = units * (blockIdx.x + 1) / n;
+    const int shares = (int)min((long long)n, units);          // (none of them empty)
+    const long long u0 = units * blockIdx.x / shares, u1 = units * (blockIdx.x + 1) / shares;
     if (lane == 0) {
         PromptWalk &w = sm.walk[warp];
-        w.left = u1 - u0;
+        w.left = (int)blockIdx.x < shares ? u1 - u0 : 0;
         long long at = u0;
         int b = 0;
-        while (b < seqs && at >= sm.plan[b]) at -= sm.plan[b++];
+        while (b < seqs && at >= sm.plan[b]) at -= sm.plan[b++];       // (b = seqs behind the last share)
         w.seq = b;
         if (b < seqs && w.left > 0) {
             const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
@@ -322,12 +323,7 @@ attend_prompt_kernel(const AttArgs A, int split) {
         (reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort = &sm.abort;
-    if (threadIdx.x == 0) {
-        AttMeta m;
-        m.units = 0;
-        m.last = m.rows = m.row0 = m.head = m.token0 = m.pad = 0;
-        A.meta[blockIdx.x] = m;
-    }
+    if (threadIdx.x == 0) A.meta[blockIdx.x] = AttMeta{};
     if (A.few) {
         // nothing to do where every sequence has few rows
         bool any = false;
@@ -553,16 +549,14 @@ attend_prompt_kernel(const AttArgs A, int split) {
                 }
                 if (threadIdx.x == 0 && it.t0 == 0) {
                     // the last share with a piece of this item: the one of its last tile
-                    const long long units = sm.plan_units, n = gridDim.x;
+                    const long long units = sm.plan_units, n = min((long long)gridDim.x, units);
                     const long long end = units * (blockIdx.x + 1) / n - it.t1 + it.steps;
                     AttMeta mt;
-                    mt.units = units;
                     mt.last = (int)min(n - 1, (end * n - 1) / units);
                     mt.rows = it.rows[0] + it.rows[1];
                     mt.row0 = it.row0;
                     mt.head = it.head;
                     mt.token0 = it.s.s0;
-                    mt.pad = 0;
                     A.meta[blockIdx.x] = mt;
                 }
                 tc::fence_before();
@@ -737,7 +731,7 @@ attend_prompt_kernel(const AttArgs A, int split) {
 // channels.
 template <int D>
 __global__ void __launch_bounds__(128)
-attend_prompt_join_kernel(const AttArgs A, int n) {
+attend_prompt_join_kernel(const AttArgs A) {
     grid_dependency_begin();
     constexpr int COLS = D / 16;                 // of 4 channels, per warp
     const AttMeta mt = A.meta[blockIdx.x];
@@ -745,14 +739,10 @@ attend_prompt_join_kernel(const AttArgs A, int n) {
     if ((int)(32 * blockIdx.y) >= mt.rows) return;
     const bool valid = row < mt.rows;
     const int i0 = blockIdx.x, last = mt.last;
-    const auto piece = [&](int i) {             // slot, or -1
-        if (mt.units < n && i > i0 && mt.units * i / n >= mt.units * (i + 1) / n) return -1;
-        return 2 * i + (i == i0 ? 1 : 0);
-    };
+    const auto piece = [&](int i) { return 2 * i + (i == i0 ? 1 : 0); };     // its slot
     float mx = -INFINITY;
     for (int i = i0; i <= last; ++i) {
-        const int k = piece(i);
-        if (k >= 0 && valid) mx = max_nan(mx, A.part_ml[k * kPromptRows + row].x);
+        if (valid) mx = max_nan(mx, A.part_ml[piece(i) * kPromptRows + row].x);
     }
     const float base = mx == -INFINITY ? 0.0f : mx;
     float4 acc[COLS];
@@ -760,8 +750,8 @@ attend_prompt_join_kernel(const AttArgs A, int n) {
     for (int c = 0; c < COLS; ++c) acc[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
     for (int i = i0; i <= last; ++i) {
+        if (!valid) continue;
         const int k = piece(i);
-        if (k < 0 || !valid) continue;
         const float2 ml = A.part_ml[k * kPromptRows + row];
         const float f = ex2(ml.x - base);
         sum = fmaf(ml.y, f, sum);
@@ -813,7 +803,7 @@ cudaError_t launch_attend_prompt(AttendLaunch &L, int few) {
     L.launches += split ? 2 : 1;
     e = launch_k(kern, dim3((unsigned)(split ? n : std::min(hi, n))), dim3(kPromptThreads), bytes, L.stream, A, split);
     if (e != cudaSuccess || !split) return e;
-    return launch_k(attend_prompt_join_kernel<D>, dim3((unsigned)n, kPromptRows / 32), dim3(128), 0, L.stream, A, (int)n);
+    return launch_k(attend_prompt_join_kernel<D>, dim3((unsigned)n, kPromptRows / 32), dim3(128), 0, L.stream, A);
 }
 
 template <int CODES, int GS, int G, int D>
