@@ -25,7 +25,7 @@
 // first product's result to the second's operand with movmatrix.
 //
 // Work: (sequence, cache head, tile of 8 rows) segments of 256-token units
-// (1024 in batches of short sequences), numbered through the batch; CTA i of n
+// (whole ones in batches of short sequences), numbered through the batch; CTA i of n
 // takes units [U i / n, U (i+1) / n) (found by a scan over the sequences'
 // lengths on the device, so lengths may differ freely and the call needs no
 // host copy of them).  A segment that one CTA covers is written at once; the
@@ -51,13 +51,17 @@ namespace dq {
 constexpr int kAttWarps = 8;
 constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kAttTile = 32;                       // tokens per warp step
-constexpr int kAttUnit = kAttTile * kAttWarps;     // tokens per step of a CTA, and per unit of work;
-// but where every sequence has at most this many steps, segments are whole: a
-// step takes about 1 us, writing and joining pieces 5.  One token, us, cut
-// against whole: 511 positions 10.1, 7.4 (8 heads of 128) and 12.0, 6.3 (3 of
-// 64); 1000 11.1, 10.3; 32 sequences 17.0, 13.7; 48 23.4, 23.6; 128 47.7, 45.4; 2000
-// positions 12.8, 16.0; 32 sequences 23.7, 23.0; 128 67.6, 75.5.
+constexpr int kAttUnit = kAttTile * kAttWarps;     // tokens per step of a CTA, and per unit of work
+// But where every sequence has few steps, segments are whole: up to
+// kAttWhole steps, or half of that where there are not enough segments to give
+// every second SM one.  A step takes 1 to 1.5 us, writing and joining pieces 2 to
+// 3.  One token each, 8 heads of 128, us, cut against whole: 1 sequence of 500
+// positions 8.5, 7.0, of 1000 8.8, 9.8; 4 of 1000 8.9, 12.0; 16 of 1000 14.8, 13.5;
+// 32 17.1, 13.9; 128 47.4, 45.6; 16 of 1500 14.6, 14.8; 48 26.3, 32.5.
 constexpr int kAttWhole = 4;
+__host__ __device__ inline int att_whole(int64_t segments) {
+    return (segments >= 74 ? kAttWhole : kAttWhole / 2) * kAttUnit;
+}
 constexpr int kAttCtas = 2 * 148;
 
 // Sequences of up to 32 query rows (new tokens x heads of a group) are this
@@ -350,13 +354,14 @@ attend_split_kernel(const AttArgs A) {
     const int heads = A.cache.heads, seqs = A.batch.seqs;
 
     // ---- this CTA's share: units [u0, u1) of the batch
+    const int most = att_whole((int64_t)seqs * heads);
     bool longer = false;
     for (int b = tid; b < seqs; b += kAttThreads) {
         const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
         if (!s.ok && me == 0) atomicOr(A.status, STATUS_INDEX);
-        longer |= s.len > kAttWhole * kAttUnit;
+        longer |= s.len > most;
     }
-    const int unit = __syncthreads_or(longer) ? kAttUnit : kAttWhole * kAttUnit;
+    const int unit = __syncthreads_or(longer) ? kAttUnit : most;
     long long mine = 0, total = 0;
     for (int b = tid; b < seqs; b += kAttThreads) {
         const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
@@ -931,7 +936,8 @@ cudaError_t launch_attend_split(AttendLaunch &L, int few) {
     if (e != cudaSuccess) return e;
     L.launches += 1;
     // (nothing is cut where no sequence can be longer)
-    if ((int64_t)L.batch.max_pages * L.cache.page_size <= kAttWhole * kAttUnit) return cudaSuccess;
+    if ((int64_t)L.batch.max_pages * L.cache.page_size <= att_whole((int64_t)L.batch.seqs * L.cache.heads))
+        return cudaSuccess;
     L.launches += 1;
     return launch_k(attend_join_kernel<D>, dim3(kAttCtas, Sh::ROWS), dim3(128), 0, L.stream, A);
 }
