@@ -38,7 +38,7 @@
 // TB/s.  Bound by instruction issue (65% of the slots, 16 warps a SM of 128
 // registers each, 511 warp instructions per 32 positions); the products alone
 // would take 60 us of the first, the codes 65 at the memory's rate.  A call of
-// one token over 511 positions (3 heads of 64) takes 6.7 us, the latency of two
+// one token over 511 positions (3 heads of 64) takes 6.3 us, the latency of two
 // steps.
 #pragma once
 
