@@ -248,6 +248,25 @@ __device__ __forceinline__ void nibble_pairs(uint32_t x, uint32_t (&out)[4], uin
     }
 }
 
+// Two tokens' words of 8 codes, channels 8 c .. of a block of 32, where the
+// lanes of a quad (c = 0..3) hold the first group of 16 in its lower half and
+// the second in its upper: lanes c and c + 2 exchange halves, so that each
+// holds 4 channels of both groups, at 8 c (upper lanes: 8 c - 12) and 8 c + 16
+// (8 c + 4).  The halves of the word become the first and the last two results
+// of the conversion: the two groups.
+template <int CODES>
+__device__ __forceinline__ void k_order(uint32_t &a, uint32_t &b, bool upper) {
+    const uint32_t give = prmt(a, b, upper ? 0x5410u : 0x7632u);
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 2);
+    if constexpr (CODES == CODES_INT4) {            // (nibbles i and i + 4 go together)
+        a = prmt(a, got, upper ? 0x3524u : 0x5140u);
+        b = prmt(b, got, upper ? 0x3726u : 0x7160u);
+    } else {
+        a = prmt(a, got, upper ? 0x3254u : 0x5410u);
+        b = prmt(b, got, upper ? 0x3276u : 0x7610u);
+    }
+}
+
 // A token's group scales in shared memory: SB bytes as words.
 template <int SB>
 struct ScaleWords {
@@ -350,6 +369,7 @@ attend_split_kernel(const AttArgs A) {
     __shared__ int s_seq;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
+    const bool upper = c >= 2;
     const int me = blockIdx.x;
     const int heads = A.cache.heads, seqs = A.batch.seqs;
 
@@ -505,10 +525,19 @@ attend_split_kernel(const AttArgs A) {
         uint4 raw[NJ];
         const int row = row0 + r, tok = row / A.group;
         const uint16_t *p = A.q + (s.s0 + tok) * A.q_token +
-                            (int64_t)(head * A.group + row - tok * A.group) * A.q_head + 8 * c;
+                            (int64_t)(head * A.group + row - tok * A.group) * A.q_head;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            raw[j] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * j)) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < NJ; ++j) {
+            raw[j] = make_uint4(0, 0, 0, 0);
+            if (r >= rows) continue;
+            if constexpr (G == 16) {                            // 4 channels of each group (k_order)
+                const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p + 32 * j + (upper ? 8 * c - 12 : 8 * c)));
+                const uint2 b = __ldg(reinterpret_cast<const uint2 *>(p + 32 * j + (upper ? 8 * c + 4 : 8 * c + 16)));
+                raw[j] = make_uint4(a.x, a.y, b.x, b.y);
+            } else {
+                raw[j] = __ldg(reinterpret_cast<const uint4 *>(p + 32 * j + 8 * c));
+            }
+        }
         int64_t first_rows[RING];
 #pragma unroll
         for (int i = 0; i < RING; ++i) first_rows[i] = next_row();
@@ -544,7 +573,10 @@ attend_split_kernel(const AttArgs A) {
             }
             if constexpr (CODES == CODES_INT4) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) qf[j][k] = f16x2_rn(x[k], x[k + 4]);
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (G == 16) qf[j][k] = f16x2_rn(x[k + (k & 2)], x[k + (k & 2) + 2]);
+                    else qf[j][k] = f16x2_rn(x[k], x[k + 4]);
+                }
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) qf[j][k] = f16x2_rn(x[2 * k], x[2 * k + 1]);
@@ -616,6 +648,7 @@ attend_split_kernel(const AttArgs A) {
 #pragma unroll
                     for (int jj = 0; jj < 2; ++jj) {
                         uint32_t x[4], y[4];
+                        if constexpr (G == 16) k_order<CODES>(w[2 * jj], w[2 * jj + 1], upper);
                         if constexpr (CODES == CODES_INT4) {
                             int4_halves(w[2 * jj], x);
                             int4_halves(w[2 * jj + 1], y);
@@ -625,14 +658,12 @@ attend_split_kernel(const AttArgs A) {
                         }
                         const uint32_t(&q)[4] = qf[j + jj];
                         if constexpr (G == 16) {
-                            // lanes 0, 1 of a quad hold the first group's channels, 2, 3 the second's
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
-                                const bool on = (c >> 1) == half;
                                 const int g = 2 * (j + jj) + half;
                                 float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                mma_f16(d, x[0], y[0], x[1], y[1], on ? q[0] : 0u, on ? q[1] : 0u);
-                                mma_f16(d, x[2], y[2], x[3], y[3], on ? q[2] : 0u, on ? q[3] : 0u);
+                                mma_f16(d, x[2 * half], y[2 * half], x[2 * half + 1], y[2 * half + 1], q[2 * half],
+                                        q[2 * half + 1]);
                                 const float s0 = sk[g * kAttTile], s8 = sk[g * kAttTile + 8];
                                 sc[mb][0] = fmaf(d[0], s0, sc[mb][0]);
                                 sc[mb][1] = fmaf(d[1], s0, sc[mb][1]);
