@@ -67,7 +67,7 @@ constexpr int kAttCtas = 2 * 148;
 // Sequences of up to 32 query rows (new tokens x heads of a group) are this
 // file's, longer ones the tcgen05 kernel's, which takes 256 rows at a time.
 // 8 sequences of 8 cache heads, D = 128: 32 rows each over 4001 positions 31
-// us (MXFP4) and 37 (NVFP4) here against 40 there, over 16000 87 and 112
+// us (MXFP4) and 35 (NVFP4) here against 40 there, over 16000 87 and 101
 // against 91 and 97; 16 rows 22 to 69 us against 39 to 96.
 constexpr int kAttFew = 32;
 enum { ATT_FEW = 1, ATT_MANY = 2 };
@@ -582,8 +582,9 @@ attend_split_kernel(const AttArgs A) {
                 for (int k = 0; k < 4; ++k) qf[j][k] = f16x2_rn(x[2 * k], x[2 * k + 1]);
             }
         }
-        // (above zero, so that a masked -inf stays -inf)
-        const float f = fmaxf(A.scale_log2 * pow2f(e - 13), 1e-37f);
+        // (above zero, so that a masked -inf stays -inf; a finite score times the
+        // smallest float32 is below 5e-7)
+        const float f = fmaxf(A.scale_log2 * pow2f(e - 13), __uint_as_float(1));
         fac[0] = __shfl_sync(0xffffffffu, f, 8 * c);         // row 2c of the tile
         fac[1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);     // row 2c + 1
 #pragma unroll

@@ -443,7 +443,8 @@ attend_prompt_kernel(const AttArgs A, int split) {
                     float f[2], ev[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        // (above zero, so that a masked -inf stays -inf)
+                        // (above zero, so that a masked -inf stays -inf; scores here are
+                        // below 2^37)
                         f[c] = fmaxf(fac * sm.kf[slot][quarter + c], 1e-37f);
                         ev[c] = sm.ve[slot][quarter + c];
                     }

@@ -118,12 +118,13 @@ DQ_API dq_status dq_kv_read(void *k, int64_t k_token, int64_t k_head, void *v, i
  * 8; 16-byte aligned; `out` does not overlap q.  Scores, softmax statistics
  * and sums are float32.  scale: finite, > 0.
  * Operands of the products are fp16, scaled by powers of two: queries per
- * row, what a product takes of values (and, above 8 query rows per sequence,
+ * row, what a product takes of values (and, above 32 query rows per sequence,
  * keys) per 32 positions, so that values 2^-24 below the largest group scale
  * of their 32 positions, or queries 2^-38 below their row's largest, count as
- * zero.  A query row with a NaN gives NaN; a NaN or infinite group scale at a
- * position of a sequence makes that sequence's rows of that head undefined,
- * and no others.
+ * zero.  Keys may be up to 2^100 in magnitude (scores are formed with queries
+ * scaled up to 2^14).  A query row with a NaN gives NaN; a NaN or infinite
+ * group scale at a position of a sequence makes that sequence's rows of that
+ * head undefined, and no others.
  * Workspace: dq_kv_attention_workspace bytes, 256-byte aligned, no
  * initialisation; calls that may overlap on the device need one each. */
 DQ_API dq_status dq_kv_attention_workspace(int64_t tokens, int32_t q_heads, int32_t heads,
