@@ -36,8 +36,8 @@
 // Scores are taken in steps of 64 positions, two steps' columns in turn, so
 // that the products of one step run during the softmax of the next (one step
 // of 128: 1.13 against 1.07 ms).  Measured (64 query over 8 cache heads, D =
-// 128, NVFP4): 2 sequences of 1000 new tokens over 16384 positions 971 us, 1.02
-// PFLOP/s; 2048 new tokens alone (32 query heads, MXFP4) 54 us, 0.63 PFLOP/s.
+// 128, MXFP4): 2 sequences of 1000 new tokens over 16384 positions 952 us, 1.04
+// PFLOP/s; 2048 new tokens alone (32 query heads, MXFP4) 55 us, 0.62 PFLOP/s.
 // Scores 64 columns wide run at two thirds of the tensor core's rate, so the
 // products fill 55% of its time; exponentials fill 44% of theirs.  More warps
 // (eight that expand codes, or two softmax teams) were slower, 1.2 ms: the
@@ -54,7 +54,9 @@ constexpr int kPromptTile = 128;                 // positions of a tile of keys 
 constexpr int kPromptStep = 64;                  // positions of a step of the softmax
 constexpr int kPromptThreads = 448;
 constexpr int kPromptCtas = 148;
-constexpr int kPromptPlan = 1024;                // sequences that a split is planned for
+constexpr int kPromptPlan = 64;                  // sequences, and
+constexpr int kPromptRounds = 8;                 // rounds of the grid, that cutting is planned for
+constexpr int kPromptItem = 2;                   // position tiles that an item costs beside its own
 constexpr int kPromptJoin = 6;                   // position tiles that cutting items costs a CTA
 constexpr int kPromptK0 = 12;                    // fp16 code x scale: at most 7 * 2^13
 
@@ -76,7 +78,8 @@ struct PromptItem {
 // tiles from the last (longest, when causal) to the first, all heads of each;
 // rounds of the grid run forwards and backwards in turn, so that long and
 // short ones pair up.  Or (left >= 0) an equal share of all position tiles in
-// that order, its first and last item cut where need be.
+// that order (and of kPromptItem more behind each item's, for its beginning
+// and end), its first and last item cut where need be.
 struct PromptWalk {
     int seq, round, tile, head, t;
     long long first, left;
@@ -88,6 +91,12 @@ struct PromptWalk {
         skip(A, report);
         if ((threadIdx.x & 31) == 0) step(A);
         __syncwarp();
+        // a share may begin behind an item's last tile
+        if (it.seq >= 0 && it.t0 == it.t1 && it.steps > 0) {
+            skip(A, report);
+            if ((threadIdx.x & 31) == 0) step(A);
+            __syncwarp();
+        }
         return it.seq >= 0;
     }
     // row tile pairs of a sequence (none of one that the other kernel takes)
@@ -164,12 +173,12 @@ struct PromptWalk {
         }
         if (tile < 0) tile = tiles(A, s) - 1;              // a new sequence
         fill(A, s, tile, head);
-        const int take = (int)min(left, (long long)max(it.steps, 1) - t);
-        it.t0 = t;
+        const int len = max(it.steps, 1) + kPromptItem, take = (int)min(left, (long long)len - t);
+        it.t0 = min(t, it.steps);
         it.t1 = min(t + take, it.steps);
         left -= take;
         t += take;
-        if (t >= it.steps) {
+        if (t >= len) {
             t = 0;
             if (++head == A.cache.heads) {
                 head = 0;
@@ -196,7 +205,7 @@ struct __align__(1024) PromptSmem {
     // keys, E and 2^-E of the values
     float kf[8][4], ve[8][4], vi[8][4];
     PromptWalk walk[14];                         // of each warp
-    long long plan_units, plan_items;
+    unsigned long long plan_units, plan_items, plan_most;
     long long plan[kPromptPlan];                 // position tiles of each sequence
     uint32_t tmem;
     int abort;
@@ -261,31 +270,54 @@ __host__ __device__ constexpr int prompt_order(int p) {
 }
 
 // Whether this call's items are cut into equal shares, and where this CTA's
-// share begins.  Whole items take ceil(items / CTAs) rounds of the mean item;
-// shares take the mean load and kPromptJoin tiles for writing and joining the
-// pieces (256 rows of float32 each: about 12 us, measured as two to four
-// position tiles a CTA; items are only cut where that leaves a gain).
+// share begins.  In tiles, whole items take what the CTA with the most of them
+// has; shares the mean and kPromptJoin for writing and joining the pieces (256
+// rows of float32 each).  MXFP4, 32 query over 8 heads of 128, us, whole
+// against cut: 512 new tokens over 8192 148, 89; 128 over 2048 47, 31; 4 x 512
+// over 4096 150, 137; 2 x 1000 over 16384 (64 query heads) 1071, 952; 300 over
+// 20000 (8 query heads) 342, 67; 1000 over 1000 (9 over 3 heads of 64) 23.5,
+// 21.6; 16 x 100 over 3000 82, 89; 4096 over 4096 165, and 403 before an item's
+// beginning and end counted.
 template <class Smem>
 __device__ __forceinline__ void prompt_plan(const AttArgs &A, Smem &sm, int warp, int lane) {
     const int seqs = A.batch.seqs, heads = A.cache.heads, n = gridDim.x;
+    const auto length = [&](const KvSeq &s, int tile) { return max(1, PromptWalk::span(A, s, tile)) + kPromptItem; };
     __syncthreads();                             // (the sums are zero)
     for (int b = warp; b < seqs; b += kPromptThreads / 32) {
         const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
         if (!s.ok && blockIdx.x == 0 && lane == 0) atomicOr(A.status, STATUS_INDEX);
         const int tiles = PromptWalk::tiles(A, s);
         long long sum = 0;
-        for (int i = lane; i < tiles; i += 32) sum += max(1, PromptWalk::span(A, s, i));
+        for (int i = lane; i < tiles; i += 32) sum += length(s, i);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) {
             sm.plan[b] = sum * heads;
-            atomicAdd(reinterpret_cast<unsigned long long *>(&sm.plan_units), (unsigned long long)(sum * heads));
-            atomicAdd(reinterpret_cast<unsigned long long *>(&sm.plan_items), (unsigned long long)tiles * heads);
+            atomicAdd(&sm.plan_units, (unsigned long long)(sum * heads));
+            atomicAdd(&sm.plan_items, (unsigned long long)tiles * heads);
         }
     }
     __syncthreads();
     const long long units = sm.plan_units, items = sm.plan_items;
-    if (items == 0 || (items + n - 1) / n * units * n <= items * (units + (long long)kPromptJoin * n)) return;
+    if (items == 0 || items > (long long)kPromptRounds * n) return;
+    for (int i = threadIdx.x; i < n; i += kPromptThreads) {
+        // the whole items of CTA i (as PromptWalk::index)
+        long long load = 0, first = 0;
+        int b = 0;
+        KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
+        for (int r = 0; (long long)r * n < items; ++r) {
+            const long long idx = (long long)r * n + ((r & 1) ? n - 1 - i : i);
+            if (idx >= items) break;
+            while (idx >= first + (long long)PromptWalk::tiles(A, s) * heads) {
+                first += (long long)PromptWalk::tiles(A, s) * heads;
+                s = kv_seq(A.batch, A.cache.page_size, A.tokens, ++b);
+            }
+            load += length(s, PromptWalk::tiles(A, s) - 1 - (int)((idx - first) / heads));
+        }
+        atomicMax(&sm.plan_most, (unsigned long long)load);
+    }
+    __syncthreads();
+    if ((long long)sm.plan_most * n <= units + (long long)kPromptJoin * n) return;
     // the place of unit u0, by one thread of each warp for its own walk
     const int shares = (int)min((long long)n, units);          // (none of them empty)
     const long long u0 = units * blockIdx.x / shares, u1 = units * (blockIdx.x + 1) / shares;
@@ -299,11 +331,11 @@ __device__ __forceinline__ void prompt_plan(const AttArgs &A, Smem &sm, int warp
         if (b < seqs && w.left > 0) {
             const KvSeq s = kv_seq(A.batch, A.cache.page_size, A.tokens, b);
             int tile = PromptWalk::tiles(A, s) - 1;
-            long long len = max(1, PromptWalk::span(A, s, tile));
+            long long len = length(s, tile);
             while (at >= len * heads) {
                 at -= len * heads;
                 --tile;
-                len = max(1, PromptWalk::span(A, s, tile));
+                len = length(s, tile);
             }
             w.tile = tile;
             w.head = (int)(at / len);
@@ -356,7 +388,7 @@ attend_prompt_kernel(const AttArgs A, int split) {
         w.left = -1;
     }
     if (threadIdx.x == 0) {
-        sm.plan_units = sm.plan_items = 0;
+        sm.plan_units = sm.plan_items = sm.plan_most = 0;
     }
     const PromptItem &it = sm.walk[warp].it;
     if (warp == 12) tc::tmem_alloc<512>(&sm.tmem);
@@ -800,7 +832,7 @@ cudaError_t launch_attend_prompt(AttendLaunch &L, int few) {
     const int64_t hi = ((rows + kPromptRows - 1) / kPromptRows + seqs - 1) * heads;
     const int64_t longest = ((int64_t)L.batch.max_pages * L.cache.page_size + kPromptTile - 1) / kPromptTile;
     const double loss = lo == 0 ? 0.0 : seqs == 1 ? (double)((lo + n - 1) / n * n) / lo - 1.0 : (double)(n - 1) / lo;
-    const int split = seqs <= kPromptPlan && longest > 1 && loss > (double)kPromptJoin * n / (hi * longest);
+    const int split = seqs <= kPromptPlan && longest > 1 && lo <= kPromptRounds * n && loss > (double)kPromptJoin * n / (hi * longest);
     L.launches += split ? 2 : 1;
     e = launch_k(kern, dim3((unsigned)(split ? n : std::min(hi, n))), dim3(kPromptThreads), bytes, L.stream, A, split);
     if (e != cudaSuccess || !split) return e;

@@ -283,7 +283,8 @@ def test_attention_prompts(name, G, dim, seqs):
 
 @pytest.mark.parametrize("name,G", [("int4_bf16", 64), ("mxint4", 32), ("mxfp4", 32), ("nvfp4_ts1", 16)])
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("seqs,group", [([(40, 6000)], 4), ([(300, 2500), (0, 700), (3, 0), (70, 50)], 2)])
+@pytest.mark.parametrize("seqs,group", [([(40, 6000)], 4), ([(300, 2500), (0, 700), (3, 0), (70, 50)], 2),
+                                        ([(700, 700), (300, 100), (260, 1500)], 2)])
 def test_attention_prompts_cut_and_joined(name, G, dim, seqs, group):
     """Few row tiles over many positions: shares of the grid begin and end
     inside them.  Row tiles that do not fill the 256 rows, rows that see
