@@ -11,9 +11,11 @@
 // group of G elements spans G / 8 neighbouring lanes and its maximum is a
 // shuffle butterfly, as in the activation mode of the tile kernel, whose
 // quantizer (Quant::run) makes the decisions.  The sum of squares is added
-// per thread in element order, then over lanes and warps in a fixed order.
-// 32768 rows of 8192 with a residual, MXFP8 E5M2: 347 us, 5.4 TB/s, 83% of a
-// copy's rate.
+// per thread in element order, then over lanes and (in 64 bits) warps in a
+// fixed order.
+// 32768 rows of 8192 with a residual, MXFP8 E5M2: 350 us, 5.4 TB/s, 82% of a
+// copy's rate (347 with the last sums and the root in float32, where a group
+// more often lands on the other side of a rounding than the exact y's).
 #include <cuda_runtime.h>
 
 #include "dq_launch.h"
@@ -32,6 +34,7 @@ struct NormArgs {
     int weight_f32;
     const float *b;
     float eps;
+    double per_k;            // 1 / K
     int64_t tokens;
     int K;
     uint16_t *res_out;
@@ -138,19 +141,28 @@ __device__ __forceinline__ void finish_chunk(const NormArgs &A, int64_t row, int
     }
 }
 
-// Sum over the CTA in a fixed order (lanes by butterfly, then warps in turn);
-// every thread gets it.
-__device__ __forceinline__ float block_sum(float v, float *part) {
+// Sum over the CTA in a fixed order (lanes by butterfly, then warps); every
+// thread gets it.  The warps' sums are added in 64 bits: the last few
+// additions hold most of the sum's rounding.
+__device__ __forceinline__ double block_sum(float v, float *part) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     const int nw = blockDim.x >> 5;
     if (nw == 1) return v;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = (int)(threadIdx.x & 31) < nw ? part[threadIdx.x & 31] : 0.0f;
+    double d = (int)(threadIdx.x & 31) < nw ? part[threadIdx.x & 31] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    return d;
+}
+
+// 1 / sqrt(v) to little more than half a step: a float32 estimate and one
+// Newton step whose residual is formed in 64 bits.
+__device__ __forceinline__ float rsqrt_near(double v) {
+    const float r = 1.0f / sqrtf((float)v);
+    const double d = fma(v * (double)r, (double)r, -1.0);
+    return fmaf(-0.5f * r, (float)d, r);
 }
 
 // C > 0: a row is at most C * blockDim.x chunks, held in registers.
@@ -184,10 +196,10 @@ rmsnorm_quant_kernel(const NormArgs A) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) ss = fmaf(h[i][k].y, h[i][k].y, fmaf(h[i][k].x, h[i][k].x, ss));
     }
-    ss = block_sum(ss, part);
-    if (threadIdx.x == 0 && (__float_as_uint(ss) & 0x7F800000u) == 0x7F800000u)
+    const double sum = block_sum(ss, part);
+    if (threadIdx.x == 0 && !(sum <= 3.4028234663852886e38))
         atomicOr(A.status, STATUS_NONFINITE);
-    const float inv = 1.0f / sqrtf(ss / (float)A.K + A.eps);
+    const float inv = rsqrt_near(fma(sum, A.per_k, (double)A.eps));
 #pragma unroll
     for (int i = 0; i < loops; ++i) {
         const int c = (int)threadIdx.x + i * (int)blockDim.x;
@@ -218,6 +230,7 @@ cudaError_t launch_g(const NormLaunch &L) {
     A.eps = L.eps;
     A.tokens = L.tokens;
     A.K = (int)L.K;
+    A.per_k = 1.0 / (double)L.K;
     A.res_out = static_cast<uint16_t *>(L.residual_out);
     A.res_out_stride = L.res_out_stride;
     A.codes = L.out_codes;
