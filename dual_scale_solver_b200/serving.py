@@ -9,6 +9,12 @@ A cache is the tuple (k_codes, k_scales, v_codes, v_scales); a batch is
 (starts, kv_lens, block_table), int32 device tensors: sequence s owns the
 token rows starts[s] .. starts[s+1] - 1, its last new ones, at the end of
 kv_lens[s] positions, position p of it in page block_table[s, p // page_size].
+
+What a call allocates belongs to the stream that it runs on (memory that an
+earlier call on another stream still uses is not handed to it), and results
+may also be used and dropped on the stream that is current at the call.  With
+an explicit ``stream`` the caller orders that stream behind the work that
+makes the inputs, and its reads of the results behind that stream.
 """
 from __future__ import annotations
 
@@ -87,6 +93,18 @@ def _device(tensors):
     return d
 
 
+def _fresh(shape, strides, dtype, device, stream):
+    """A tensor for a call on ``stream``, from that stream's pool: the current
+    stream's may hand out memory that its pending kernels still use, which
+    ``stream`` does not wait for."""
+    if stream is None:
+        return _new(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = _new(shape, strides, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _call(device, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current; the stream defaults
     to that device's current one."""
@@ -143,14 +161,14 @@ def add_rmsnorm_quant(x, weight, fmt, residual=None, b=None, eps=1e-5, codes=Non
             raise ValueError("residual: the shape of x")
         rp = residual.data_ptr()
         if residual_out is None:
-            residual_out = _new((tokens, K), (K, 1), dtype=_bf16, device=x.device)
+            residual_out = _fresh((tokens, K), (K, 1), _bf16, x.device, stream)
     if residual_out is not None:
         shape, (os,) = _rows(residual_out, "residual_out")
         if shape != (tokens, K):
             raise ValueError("residual_out: the shape of x")
         op = residual_out.data_ptr()
     if codes is None or gscales is None:
-        codes, gscales = _outputs(tokens, K, fmt, x.device, codes, gscales)
+        codes, gscales = _outputs(tokens, K, fmt, x.device, codes, gscales, stream)
     if not (codes.is_contiguous() and gscales.is_contiguous()):
         raise ValueError("codes and gscales: contiguous")
     status = _call(dev, stream, _lib().dq_add_rmsnorm_quant, x.data_ptr(), xs, rp, rs,
@@ -164,17 +182,17 @@ def add_rmsnorm_quant(x, weight, fmt, residual=None, b=None, eps=1e-5, codes=Non
 _BITS = (4, 4, 8, 8, 8, 6, 6)           # of a code, by DQ_CODES_*
 
 
-def _outputs(tokens, K, fmt, device, codes, gscales):
+def _outputs(tokens, K, fmt, device, codes, gscales, stream):
     if not 0 <= fmt.codes < 7 or fmt.group <= 0 or K % fmt.group:
         from . import DqError
         raise DqError(-2 if 0 <= fmt.codes < 7 and fmt.group > 0 else -3, "dq_add_rmsnorm_quant")
     if codes is None:
         n = K * _BITS[fmt.codes] // 8
-        codes = _new((tokens, n), (n, 1), dtype=torch.uint8, device=device)
+        codes = _fresh((tokens, n), (n, 1), torch.uint8, device, stream)
     if gscales is None:
         n = K // fmt.group
-        gscales = _new((tokens, n), (n, 1), dtype=torch.int16 if fmt.group_scale == 0 else torch.uint8,
-                       device=device)
+        gscales = _fresh((tokens, n), (n, 1), torch.int16 if fmt.group_scale == 0 else torch.uint8,
+                         device, stream)
     return codes, gscales
 
 
@@ -247,11 +265,11 @@ def kv_read(cache, starts, kv_lens, block_table, fmt, tokens, k=None, v=None, st
     they are (undefined in tensors allocated here)."""
     _, heads, _, half = cache[0].shape
     if k is None:
-        k = _new((tokens, heads, 2 * half), (2 * heads * half, 2 * half, 1), dtype=_bf16,
-                 device=cache[0].device)
+        k = _fresh((tokens, heads, 2 * half), (2 * heads * half, 2 * half, 1), _bf16, cache[0].device,
+                   stream)
     if v is None:
-        v = _new((tokens, heads, 2 * half), (2 * heads * half, 2 * half, 1), dtype=_bf16,
-                 device=cache[0].device)
+        v = _fresh((tokens, heads, 2 * half), (2 * heads * half, 2 * half, 1), _bf16, cache[0].device,
+                   stream)
     if k.shape[0] != tokens:
         raise ValueError("k: [tokens, heads, head_dim]")
     _copy(_lib().dq_kv_read, "dq_kv_read", k, v, cache, starts, kv_lens, block_table, fmt, stream)
@@ -289,16 +307,14 @@ def kv_attention(q, cache, starts, kv_lens, block_table, fmt, scale=None, causal
     tokens, q_heads, _ = shape
     if out is None:
         ot, oh = q_heads * dim, dim
-        out = _new(shape, (ot, oh, 1), dtype=_bf16, device=q.device)
+        out = _fresh(shape, (ot, oh, 1), _bf16, q.device, stream)
     else:
         so, (ot, oh) = _rows(out, "out")
         if so != shape:
             raise ValueError("out: the shape of q")
     if ws is None:
-        ws = _new((kv_attention_workspace(tokens, q_heads, heads, dim, seqs),), (1,), dtype=torch.uint8,
-                  device=q.device)
-        if stream is not None:
-            ws.record_stream(stream)
+        ws = _fresh((kv_attention_workspace(tokens, q_heads, heads, dim, seqs),), (1,), torch.uint8, q.device,
+                    stream)
     status = _call(dev, stream, _lib().dq_kv_attention, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
                    tokens, q_heads, 1.0 / math.sqrt(dim) if scale is None else scale, 1 if causal else 0,
                    c, b, byref(fmt), ws.data_ptr(), ws.nbytes)
