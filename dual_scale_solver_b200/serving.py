@@ -143,7 +143,8 @@ def add_rmsnorm_quant(x, weight, fmt, residual=None, b=None, eps=1e-5, codes=Non
     is written to ``residual_out`` (allocated when a residual is given and
     none is passed; pass ``residual`` itself to update it in place) rounded
     to bf16; the norm uses the unrounded float32 sum.  weight: [K] float32 or
-    bf16; b: [K] float32 (the solver's inverse column scales) or None."""
+    bf16; b: [K] float32 (the solver's inverse column scales) or None.  codes,
+    gscales: buffers of exactly those sizes to write, or None."""
     dev = _device((x, weight, residual, b, codes, gscales, residual_out))
     (tokens, K), (xs,) = _rows(x, "x")
     if weight.shape != (K,) or not weight.is_contiguous():
@@ -167,10 +168,7 @@ def add_rmsnorm_quant(x, weight, fmt, residual=None, b=None, eps=1e-5, codes=Non
         if shape != (tokens, K):
             raise ValueError("residual_out: the shape of x")
         op = residual_out.data_ptr()
-    if codes is None or gscales is None:
-        codes, gscales = _outputs(tokens, K, fmt, x.device, codes, gscales, stream)
-    if not (codes.is_contiguous() and gscales.is_contiguous()):
-        raise ValueError("codes and gscales: contiguous")
+    codes, gscales = _outputs(tokens, K, fmt, x.device, codes, gscales, stream)
     status = _call(dev, stream, _lib().dq_add_rmsnorm_quant, x.data_ptr(), xs, rp, rs,
                    weight.data_ptr(), 1 if wd is _bf16 else 0, None if b is None else b.data_ptr(), eps,
                    tokens, K, byref(fmt), op, os, codes.data_ptr(), gscales.data_ptr())
@@ -183,16 +181,21 @@ _BITS = (4, 4, 8, 8, 8, 6, 6)           # of a code, by DQ_CODES_*
 
 
 def _outputs(tokens, K, fmt, device, codes, gscales, stream):
+    """codes and gscales, allocated where not given, of exactly the format's
+    size where given (the library sees addresses only)."""
     if not 0 <= fmt.codes < 7 or fmt.group <= 0 or K % fmt.group:
         from . import DqError
         raise DqError(-2 if 0 <= fmt.codes < 7 and fmt.group > 0 else -3, "dq_add_rmsnorm_quant")
+    n, size = K * _BITS[fmt.codes] // 8, 2 if fmt.group_scale == 0 else 1
     if codes is None:
-        n = K * _BITS[fmt.codes] // 8
         codes = _fresh((tokens, n), (n, 1), torch.uint8, device, stream)
+    elif codes.nbytes != tokens * n or not codes.is_contiguous():
+        raise ValueError(f"codes: {tokens} x {n} bytes, contiguous")
+    n = K // fmt.group
     if gscales is None:
-        n = K // fmt.group
-        gscales = _fresh((tokens, n), (n, 1), torch.int16 if fmt.group_scale == 0 else torch.uint8,
-                         device, stream)
+        gscales = _fresh((tokens, n), (n, 1), torch.int16 if size == 2 else torch.uint8, device, stream)
+    elif gscales.numel() != tokens * n or gscales.element_size() != size or not gscales.is_contiguous():
+        raise ValueError(f"gscales: {tokens} x {n} of {8 * size} bits, contiguous")
     return codes, gscales
 
 
