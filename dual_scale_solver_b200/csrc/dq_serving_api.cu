@@ -2,6 +2,7 @@
 // launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "dq_serving.h"
@@ -41,6 +42,27 @@ dq_status check_cache(const dq_kv_cache *c, const dq_kv_batch *b, const dq_forma
         !aligned(b->block_table, 4))
         return DQ_ERR_ALIGN;
     return DQ_OK;
+}
+
+// Whether two bf16 arrays [tokens, heads, dim] share an element.  Exact where
+// both have the same strides (interleaved slices of one array do not overlap);
+// otherwise whether their extents meet.
+bool overlap(const void *pa, int64_t token_a, int64_t head_a, const void *pb, int64_t token_b,
+             int64_t head_b, int64_t tokens, int64_t heads, int64_t dim) {
+    if (!pa || !pb) return false;
+    const auto extent = [&](int64_t token, int64_t head) { return (tokens - 1) * token + (heads - 1) * head + dim; };
+    const int64_t d = ((intptr_t)pb - (intptr_t)pa) / 2;       // (both are 16-byte aligned)
+    if (d >= extent(token_a, head_a) || -d >= extent(token_b, head_b)) return false;
+    if ((tokens > 1 && token_a != token_b) || (heads > 1 && head_a != head_b)) return true;
+    // rows i tokens and j heads apart, for each j the i that bring them closest
+    for (int64_t j = 1 - heads; j < heads; ++j) {
+        const int64_t x = d + j * head_a, near = token_a ? -x / token_a : 0;
+        for (int64_t i = near - 1; i <= near + 1; ++i) {
+            const int64_t y = x + std::min(std::max(i, 1 - tokens), tokens - 1) * token_a;
+            if (y < dim && -y < dim) return true;
+        }
+    }
+    return false;
 }
 
 // A bf16 array [tokens, heads, dim] by its strides (16-byte accesses); an
@@ -108,6 +130,10 @@ dq_status dq_add_rmsnorm_quant(const void *x, int64_t x_stride, const void *resi
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(b, 16) ||
         !aligned(residual_out, 16) || !aligned(codes, 16) || !aligned(gscales, 16))
         return DQ_ERR_ALIGN;
+    // (in place: a row's elements are read before they are written)
+    if (residual_out != x && overlap(x, x_stride, 0, residual_out, res_out_stride, 0, tokens, 1, K)) return DQ_ERR_ARG;
+    if (residual_out != residual && overlap(residual, res_stride, 0, residual_out, res_out_stride, 0, tokens, 1, K))
+        return DQ_ERR_ARG;
     NormLaunch L;
     L.status = serving_status_word();
     if (!L.status) return DQ_ERR_CUDA;

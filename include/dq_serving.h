@@ -32,7 +32,8 @@ extern "C" {
  * x, residual: bf16, `tokens` rows of K elements, rows x_stride and
  * res_stride elements apart; residual_out: bf16, rows res_out_stride apart,
  * may be the same buffer as x or residual (same stride), and may not overlap
- * them otherwise.  weight: [K] of weight_dtype
+ * them otherwise (DQ_ERR_ARG; with another stride than theirs it lies outside
+ * their extent).  weight: [K] of weight_dtype
  * (DQ_DT_F32 or DQ_DT_BF16); b: [K] float32, the inverse column scales of the
  * matrix that reads the result (dq_solve_dual_scale), or NULL for ones.
  * codes: dq_code_bytes(fmt, tokens, K) bytes; gscales [tokens, K/G]; every

@@ -1,0 +1,58 @@
+"""Outputs of the serving operators over their inputs: refused on the host,
+element by element (no GPU)."""
+import ctypes
+import itertools
+
+import pytest
+import torch
+
+import dual_scale_solver_b200 as dq
+from dual_scale_solver_b200 import serving
+
+ARG, CUDA = -1, -6
+BASE = 1 << 20                              # an address, never dereferenced
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from dual_scale_solver_b200 import build
+    build.build()
+
+
+def _status(call, refused):
+    """A call that is not refused reaches the device, which is not there."""
+    if not refused and torch.cuda.is_available():
+        return CUDA
+    return call()
+
+
+def _elements(at, token, head, tokens, heads, dim):
+    return {at + t * token + h * head + d for t in range(tokens) for h in range(heads) for d in range(dim)}
+
+
+def _norm(res, out, stride, out_stride, x=BASE + (1 << 22)):
+    f, p = dq.format_preset("mxfp4"), lambda e: None if e is None else ctypes.c_void_p(BASE + 2 * e)  # noqa: E731
+    return serving._lib().dq_add_rmsnorm_quant(ctypes.c_void_p(x), 64, p(res), stride, ctypes.c_void_p(BASE + (1 << 23)),
+                                               1, None, 1e-5, 3, 64, ctypes.byref(f), p(out), out_stride,
+                                               ctypes.c_void_p(BASE + (1 << 24)), ctypes.c_void_p(BASE + (1 << 25)), None)
+
+
+@pytest.mark.parametrize("stride", [64, 72, 128, 192])
+def test_norm_residual_out_over_an_input(stride):
+    base = 4096
+    for shift in range(-4 * stride, 4 * stride + 1, 8):
+        a, b = _elements(base, stride, 0, 3, 1, 64), _elements(base + shift, stride, 0, 3, 1, 64)
+        refused = shift != 0 and bool(a & b)
+        want = ARG if refused else CUDA
+        assert _status(lambda: _norm(base, base + shift, stride, stride), refused) == want, shift
+        # over x
+        if stride == 64:
+            assert _status(lambda: _norm(None, base + shift, stride, stride, x=BASE + 2 * base), refused) == want, shift
+    # other strides: apart or refused
+    assert _norm(base, base + 64, 128, 64) == ARG
+    assert _norm(base, base + 2 * 128 + 56, 128, 64) == ARG
+    assert _status(lambda: _norm(base, base + 2 * 128 + 64, 128, 64), False) == CUDA
+    assert _status(lambda: _norm(base + 2 * 64 + 64, base, 128, 64), False) == CUDA
+    # in place over one input, and over a part of the other
+    assert _norm(base + 8, base, 64, 64, x=BASE + 2 * base) == ARG
+    assert _status(lambda: _norm(base, base, 64, 64, x=BASE + 2 * base), False) == CUDA
