@@ -86,7 +86,8 @@ dq_status kv_copy(const void *k, int64_t k_token, int64_t k_head, const void *v,
     if (tokens == 0 || batch->seqs == 0) return DQ_OK;
     if ((s = check_rows(k, k_token, k_head, tokens, cache->heads, cache->head_dim, read)) != DQ_OK) return s;
     if ((s = check_rows(v, v_token, v_head, tokens, cache->heads, cache->head_dim, read)) != DQ_OK) return s;
-    if (read && k == v) return DQ_ERR_ARG;
+    if (read && overlap(k, k_token, k_head, v, v_token, v_head, tokens, cache->heads, cache->head_dim))
+        return DQ_ERR_ARG;
     KvCopyLaunch L;
     L.status = serving_status_word();
     if (!L.status) return DQ_ERR_CUDA;

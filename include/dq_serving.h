@@ -104,7 +104,8 @@ DQ_API dq_status dq_kv_append(const void *k, int64_t k_token, int64_t k_head, co
 
 /* The values held in the cache for the batch's new tokens, code * group scale
  * rounded to bf16 (exact for E8M0 and E4M3 scales): the inverse of
- * dq_kv_append, with the same array layout (k and v may not overlap). */
+ * dq_kv_append, with the same array layout (k and v may not overlap:
+ * DQ_ERR_ARG; arrays of unequal strides lie outside each other's extent). */
 DQ_API dq_status dq_kv_read(void *k, int64_t k_token, int64_t k_head, void *v, int64_t v_token,
                             int64_t v_head, int64_t tokens, const dq_kv_cache *cache,
                             const dq_kv_batch *batch, const dq_format *fmt, dq_stream stream);

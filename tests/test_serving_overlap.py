@@ -56,3 +56,36 @@ def test_norm_residual_out_over_an_input(stride):
     # in place over one input, and over a part of the other
     assert _norm(base + 8, base, 64, 64, x=BASE + 2 * base) == ARG
     assert _status(lambda: _norm(base, base, 64, 64, x=BASE + 2 * base), False) == CUDA
+
+
+LAYOUTS = [(256, 128), (128, 3 * 128), (512, 128), (384, 192), (512, 256)]     # (token, head), 3 x 2 rows of 128
+
+
+def _places():
+    return (serving.dq_kv_cache(BASE, BASE, BASE, BASE, 8, 16, 2, 128),
+            serving.dq_kv_batch(BASE, BASE, BASE, 2, 4, 4))
+
+
+def _read(at, other, a, b):
+    f, (c, m) = dq.format_preset("mxfp4"), _places()
+    p = lambda e: ctypes.c_void_p(BASE + 2 * e)                # noqa: E731
+    return serving._lib().dq_kv_read(p(at), *a, p(other), *b, 3, ctypes.addressof(c), ctypes.addressof(m),
+                                     ctypes.byref(f), None)
+
+
+def _check_pairs(call):
+    base = 8192
+    for a, b in itertools.product(LAYOUTS, LAYOUTS):
+        one, end = _elements(base, *a, 3, 2, 128), base + 2 * a[0] + a[1] + 128
+        for shift in range(-1600, 1601, 40):
+            other = _elements(base + shift, *b, 3, 2, 128)
+            meet = base + shift < end and base < base + shift + 2 * b[0] + b[1] + 128
+            refused = bool(one & other) if a == b else meet
+            assert refused or not (one & other)
+            want = ARG if refused else CUDA
+            assert _status(lambda: call(base, base + shift, a, b), refused) == want, (a, b, shift)
+
+
+def test_read_keys_over_values():
+    _check_pairs(_read)
+    assert _read(8192, 8192, (256, 128), (512, 128)) == ARG
