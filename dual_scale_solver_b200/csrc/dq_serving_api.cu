@@ -197,7 +197,8 @@ dq_status dq_kv_attention(const void *q, int64_t q_token, int64_t q_head, void *
         ws_bytes < attend_workspace(tokens, q_heads, cache->heads, cache->head_dim, batch->seqs))
         return DQ_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return DQ_ERR_ALIGN;
-    if (out == q) return DQ_ERR_ARG;             // (rows of q are read until the call's end)
+    // (rows of q are read until the call's end)
+    if (overlap(q, q_token, q_head, out, out_token, out_head, tokens, q_heads, cache->head_dim)) return DQ_ERR_ARG;
     AttendLaunch L;
     L.status = serving_status_word();
     if (!L.status) return DQ_ERR_CUDA;

@@ -117,7 +117,8 @@ DQ_API dq_status dq_kv_read(void *k, int64_t k_token, int64_t k_head, void *v, i
  * own.  A row that sees no position (an empty sequence, or more new tokens
  * than kv_lens with causal != 0) gives zeros.  q and out: bf16 [tokens,
  * q_heads, head_dim], channels contiguous, strides in elements, multiples of
- * 8; 16-byte aligned; `out` does not overlap q.  Scores, softmax statistics
+ * 8; 16-byte aligned; `out` does not overlap q (DQ_ERR_ARG; with other strides
+ * than q's it lies outside its extent).  Scores, softmax statistics
  * and sums are float32.  scale: finite, > 0.
  * Operands of the products are fp16, scaled by powers of two: queries per
  * row, what a product takes of values (and, above 32 query rows per sequence,

@@ -89,3 +89,21 @@ def _check_pairs(call):
 def test_read_keys_over_values():
     _check_pairs(_read)
     assert _read(8192, 8192, (256, 128), (512, 128)) == ARG
+
+
+def _attend(at, other, a, b, tokens=3):
+    f, (c, m) = dq.format_preset("mxfp4"), _places()
+    p = lambda e: ctypes.c_void_p(BASE + 2 * e)                # noqa: E731
+    return serving._lib().dq_kv_attention(p(at), *a, p(other), *b, tokens, 2, 0.1, 1, ctypes.addressof(c),
+                                          ctypes.addressof(m), ctypes.byref(f), ctypes.c_void_p(BASE), 1 << 30, None)
+
+
+def test_attention_over_its_queries():
+    _check_pairs(_attend)
+    # queries that are all one row
+    assert _attend(8192, 8192 + 120, (0, 0), (256, 128)) == ARG
+    assert _attend(8192, 8192 - 512 - 128, (0, 0), (256, 128)) == ARG
+    assert _status(lambda: _attend(8192, 8192 + 128, (0, 0), (256, 128)), False) == CUDA
+    # one token: its stride does not matter
+    assert _status(lambda: _attend(8192, 8192 + 128, (1024, 256), (256, 256), tokens=1), False) == CUDA
+    assert _attend(8192, 8192 + 256, (1024, 256), (256, 256), tokens=1) == ARG
