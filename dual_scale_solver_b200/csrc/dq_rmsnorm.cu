@@ -11,12 +11,14 @@
 // group of G elements spans G / 8 neighbouring lanes and its maximum is a
 // shuffle butterfly, as in the activation mode of the tile kernel, whose
 // quantizer (Quant::run) makes the decisions.  The sum of squares is added
-// per thread in element order, then over lanes and (in 64 bits) warps in a
-// fixed order.
+// per thread in element order (at most 32 of them in float32), then over lanes
+// and (in 64 bits) warps in a fixed order.
 // 32768 rows of 8192 with a residual, MXFP8 E5M2: 350 us, 5.4 TB/s, 82% of a
 // copy's rate (347 with the last sums and the root in float32, where a group
 // more often lands on the other side of a rounding than the exact y's).
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "dq_launch.h"
 #include "dq_serving.h"
@@ -143,15 +145,16 @@ __device__ __forceinline__ void finish_chunk(const NormArgs &A, int64_t row, int
 
 // Sum over the CTA in a fixed order (lanes by butterfly, then warps); every
 // thread gets it.  The warps' sums are added in 64 bits: the last few
-// additions hold most of the sum's rounding.
-__device__ __forceinline__ double block_sum(float v, float *part) {
+// additions hold most of the sum's rounding.  T: the type of the threads' sums.
+template <typename T>
+__device__ __forceinline__ double block_sum(T v, T *part) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     const int nw = blockDim.x >> 5;
     if (nw == 1) return v;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    double d = (int)(threadIdx.x & 31) < nw ? part[threadIdx.x & 31] : 0.0f;
+    double d = (int)(threadIdx.x & 31) < nw ? part[threadIdx.x & 31] : T(0);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     return d;
@@ -167,16 +170,19 @@ __device__ __forceinline__ float rsqrt_near(double v) {
 
 // C > 0: a row is at most C * blockDim.x chunks, held in registers.
 // C == 0: any K; the row is read a second time for the quantization (from L2).
+// A thread then has K / 1024 squares, up to 2^18: its sum is taken to 64 bits
+// after each chunk, since 2^14 equal squares already lose 6e-5 in float32.
 template <int CODES, int GS, int G, int C>
 __global__ void __launch_bounds__(kNormMaxThreads)
 rmsnorm_quant_kernel(const NormArgs A) {
     grid_dependency_begin();
-    __shared__ float part[32];
+    using Sum = typename std::conditional<(C > 0), float, double>::type;
+    __shared__ Sum part[32];
     const int nch = A.K / 8;
     const int64_t row = blockIdx.x;
     constexpr int CH = C > 0 ? C : 1;
     f2 h[CH][4];
-    float ss = 0.0f;
+    Sum ss = 0;
     const int loops = C > 0 ? C : (nch + (int)blockDim.x - 1) / (int)blockDim.x;
 #pragma unroll
     for (int i = 0; i < loops; ++i) {
@@ -186,8 +192,10 @@ rmsnorm_quant_kernel(const NormArgs A) {
         for (int k = 0; k < 4; ++k) hh[k] = make_float2(0.0f, 0.0f);
         if (c < nch) load_h(A, row, c, hh);
         if constexpr (C == 0) {
+            float chunk = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ss = fmaf(hh[k].y, hh[k].y, fmaf(hh[k].x, hh[k].x, ss));
+            for (int k = 0; k < 4; ++k) chunk = fmaf(hh[k].y, hh[k].y, fmaf(hh[k].x, hh[k].x, chunk));
+            ss += chunk;
         }
     }
     if constexpr (C > 0) {
