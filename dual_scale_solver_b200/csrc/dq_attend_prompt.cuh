@@ -41,7 +41,8 @@
 // Scores 64 columns wide run at two thirds of the tensor core's rate, so the
 // products fill 55% of its time; exponentials fill 44% of theirs.  More warps
 // (eight that expand codes, or two softmax teams) were slower, 1.2 ms: the
-// registers a thread keeps fall below 96.
+// registers a thread keeps fall below 96.  At 128 each instantiation spills 5 to 9
+// of them (20 to 36 bytes).
 #pragma once
 
 #include "dq_attend.cuh"
@@ -827,6 +828,13 @@ cudaError_t launch_attend_prompt(AttendLaunch &L, int few) {
     // Whether items may be cut at all, by what the host knows (the kernel
     // decides): at least lo items of at most `longest` tiles, so whole items
     // lose at most (n - 1) / lo of the time (exactly known for one sequence).
+    // Where lo is 0 (32 rows a sequence in the mean, or fewer) there may be no
+    // item at all: batches of drafts, which are not to pay the joining kernel's
+    // launch, and mixed ones are then whole, as all batches of more than
+    // kPromptPlan sequences are.  us, whole against cut, 32 query heads over 8
+    // of 128: 8 x 5 of 4001 NVFP4 31.0, 33.5; MXFP4: 30 single tokens with a piece
+    // of 40, all over 500 positions, 30.4, 36.1, all over 2000, 76, 65; 50 over 2000
+    // with 200 over 4000 130, 94; 60 over 2000 with 300 over 20000 410, 187.
     const int64_t n = kPromptCtas, heads = L.cache.heads, seqs = L.batch.seqs, rows = L.tokens * A.group;
     const int64_t lo = std::max<int64_t>((rows - few * seqs + kPromptRows - 1) / kPromptRows, 0) * heads;
     const int64_t hi = ((rows + kPromptRows - 1) / kPromptRows + seqs - 1) * heads;

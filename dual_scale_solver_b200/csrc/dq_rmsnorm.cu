@@ -14,8 +14,9 @@
 // per thread in element order (at most 32 of them in float32), then over lanes
 // and (in 64 bits) warps in a fixed order.
 // 32768 rows of 8192 with a residual, MXFP8 E5M2: 350 us, 5.4 TB/s, 82% of a
-// copy's rate (347 with the last sums and the root in float32, where a group
-// more often lands on the other side of a rounding than the exact y's).
+// copy's rate (347 with the last sums and the root in float32).  Of these 268
+// million codes 62 to 124 are not those of the exact y (six inputs, 81 in the
+// mean; with elementary float32 operations 70 to 117, 93 in the mean).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -252,7 +253,11 @@ cudaError_t launch_g(const NormLaunch &L) {
     // flight, fewer reductions).  MXFP8, us, 8 against 32: 61 x 8192 2.8, 4.0;
     // 592 x 4096 3.8, 4.5; 1184 x 4096 6.6, 5.9; 592 x 8192 6.9, 6.0; 8192 x
     // 2048 25.2, 26.0; 8192 x 1024 11.7, 13.2; 8192 x 8192 112, 94; 32768 x 8192
-    // 429, 347 (16 elements: 409, 64: 501).
+    // 429, 347 (16 elements: 409, 64: 501).  MXFP4 with b: 592 x 4096 4.6, 4.7;
+    // 592 x 8192 9.9, 8.2; 2048 x 4096 17.2, 16.4; 8192 x 2048 26.9, 27.5; 32768 x
+    // 8192 435, 351.  NVFP4 with b: 592 x 4096 6.0, 5.6; 2048 x 4096 24.2, 18.5;
+    // 8192 x 1024 18.7, 17.8; 8192 x 2048 35.8, 30.5 (the one that the rule costs
+    // most); 32768 x 8192 762, 391.
     if (nch > kNormMaxThreads || (L.K >= 4096 && L.tokens * L.K > (1 << 22)))
         return launch_c<CODES, GS, G, 4>(L, A, round32((nch + 3) / 4));
     return launch_c<CODES, GS, G, 1>(L, A, round32(nch));

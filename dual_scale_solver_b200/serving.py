@@ -97,11 +97,12 @@ def _fresh(shape, strides, dtype, device, stream):
     """A tensor for a call on ``stream``, from that stream's pool: the current
     stream's may hand out memory that its pending kernels still use, which
     ``stream`` does not wait for."""
-    if stream is None:
+    current = None if stream is None else torch.cuda.current_stream(device)
+    if stream == current:
         return _new(shape, strides, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = _new(shape, strides, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+    t.record_stream(current)
     return t
 
 

@@ -156,3 +156,31 @@ def test_attention_close_when_cut(name, G):
     q = bf16_from(B.rng, (B.tokens, 4, 64)).cuda()
     for scale in (0.02, None):
         _check_close(B, q, cache, values, scale)
+
+
+def test_outputs_between_the_rows_of_inputs():
+    """Interleaved slices of one array share no element: they are answered,
+    and the input's rows stay as they were."""
+    B = Batch([(1, 700), (4, 257), (40, 300)], 16, 2, 64, "mxfp4", 32)
+    cache, _ = B.fill()
+    both = bf16_from(B.rng, (B.tokens, 16, 64)).cuda()
+    q, out, before = both[:, :8], both[:, 8:], both[:, :8].clone()
+    want = dq.kv_attention(before, cache, *B.device(), B.fmt)
+    dq.kv_attention(q, cache, *B.device(), B.fmt, out=out)
+    assert torch.equal(out, want) and torch.equal(q, before)
+    both = torch.zeros(B.tokens, 2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    kv = dq.kv_read(cache, *B.device(), B.fmt, B.tokens)
+    dq.kv_read(cache, *B.device(), B.fmt, B.tokens, k=both[:, 0], v=both[:, 1])
+    assert torch.equal(both[:, 0], kv[0]) and torch.equal(both[:, 1], kv[1])
+    rows = bf16_from(B.rng, (5, 3 * 256)).cuda()
+    x, r, s = rows[:, :256], rows[:, 256:512], rows[:, 512:]
+    w, f, keep = torch.ones(256, device="cuda"), dq.format_preset("mxfp4"), rows.clone()
+    want = dq.add_rmsnorm_quant(x, w, f, residual=r)
+    got = dq.add_rmsnorm_quant(x, w, f, residual=r, residual_out=s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(rows[:, :512], keep[:, :512])
+    with pytest.raises(dq.DqError):
+        dq.add_rmsnorm_quant(x, w, f, residual=r, residual_out=rows[:, 8:264])
+    fused = torch.zeros(B.tokens, 9, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(dq.DqError):                  # one head's rows in common
+        dq.kv_attention(fused[:, :8], cache, *B.device(), B.fmt, out=fused[:, 1:])
+    assert dq.last_device_status() == 0
